@@ -296,7 +296,7 @@ def _plain_plan(s):
     pool_size = count + back_ends[-1]
     pool = torch.where((j >= 0) & (at < pool_size), theirs, s["free_pages"].long())
     # pages are taken from the top, in the requests' order
-    fits = live & (total <= width * page) & (ends <= tokens)
+    fits = live & (total <= width * page) & ((ends <= tokens) | (rows == 0))
     need = torch.where(fits, (total + page - 1) // page - held, 0)
     taken = torch.cumsum(need, 0)
     granted = fits & ((need == 0) | (taken <= pool_size))
