@@ -45,6 +45,8 @@ EXPORTS = (
     "qlora_linear_workspace_bytes_ex", "qlora_linear_fwd_ex", "qlora_linear_bwd_ex",
     "qlora_linear_adapter_fwd", "qlora_linear_adapter_bwd",
     "qlora_dequantize_nf4_dq_ex",
+    "qlora_kv_plan", "qlora_build_rope", "qlora_kv_append",
+    "qlora_paged_attn_workspace_bytes", "qlora_paged_attn_fwd",
 )
 
 KERNEL_KINDS = ("quantize", "dq_encode", "dequantize", "fwd_fused", "bwd_fused", "lowrank", "wgrad",
@@ -82,6 +84,23 @@ class qlora_block(ctypes.Structure):
                 ("r", ctypes.c_int32), ("lora_scale", ctypes.c_float), ("rms_eps", ctypes.c_float),
                 ("rope_base", ctypes.c_float), ("w", qlora_nf4_weight * 7), ("A", ctypes.c_void_p * 7),
                 ("B", ctypes.c_void_p * 7), ("norm1", ctypes.c_void_p), ("norm2", ctypes.c_void_p)]
+
+
+class qlora_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("stride_page", ctypes.c_int64), ("stride_head", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
+
+
+class qlora_kv_batch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32), ("block_table", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p)]
+
+
+class qlora_rope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("turns", ctypes.c_double * 64)]
 
 
 def _load():
@@ -128,6 +147,11 @@ def _load():
         "qlora_linear_adapter_bwd": (ctypes.c_int, [W, P, P, I64, P, P, I32, F, P, P, S, P,
                                                     ctypes.POINTER(qlora_linear_opts)]),
         "qlora_block_fwd": (ctypes.c_int, [ctypes.POINTER(qlora_block), P, P, P, S, P]),
+        "qlora_kv_plan": (ctypes.c_int, [P, I32, I32, P, P, P, P, P, P]),
+        "qlora_build_rope": (ctypes.c_int, [I32, ctypes.c_double, P]),
+        "qlora_kv_append": (ctypes.c_int, [P, P, P, P, P, P, I32, P, P]),
+        "qlora_paged_attn_workspace_bytes": (S, [P, P, I32]),
+        "qlora_paged_attn_fwd": (ctypes.c_int, [P, P, P, I32, F, I32, I32, P, P, P, S, P]),
         "qlora_block_bwd": (ctypes.c_int, [ctypes.POINTER(qlora_block), P, P, P, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
@@ -453,3 +477,145 @@ def qlora_block_bwd(block: Block, x, dy, dx, dA, dB, workspace, stream=None):
     _check(lib.qlora_block_bwd(ctypes.byref(block.desc), _ptr(x), _ptr(dy), _ptr(dx),
                                ctypes.cast(pa, ctypes.c_void_p), ctypes.cast(pb, ctypes.c_void_p), _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream(stream)), "qlora_block_bwd")
+
+
+# ---- serving: paged cache, plan, append, attention --------------------------------------
+# The tensors of a call share one device, which need not be the current one;
+# work goes to `stream`, or to that device's current stream.
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _is(t, dtype, shape, device, name):
+    """A dense tensor of this type and shape on this device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class _On:
+    """Runs a call with `device` current and yields the raw stream."""
+
+    __slots__ = ("stream", "index", "before")
+
+    def __init__(self, device, stream):
+        _need(device.type == "cuda", f"need tensors on a CUDA device, got {device}")
+        if stream is not None:
+            _need(stream.device == device, f"stream of {stream.device} for tensors on {device}")
+        self.index, self.before = device.index, torch.cuda.current_device()
+        self.stream = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+    def __enter__(self):
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+class KVCache:
+    """A layer's paged cache over the caller's tensors k and v of shape
+    [num_pages, kv_heads, page_size, head_dim] (any order of the first three
+    dimensions in memory, both alike; head_dim contiguous)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        _need(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype and
+              k.device == v.device, "k and v must be alike and have four dimensions")
+        _need(k.stride(3) == 1 or k.shape[3] == 1, "the last dimension must be contiguous")
+        _need(k.dtype in (torch.bfloat16, torch.float16), f"unsupported dtype {k.dtype}")
+        self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.desc = qlora_kv_cache(k.data_ptr(), v.data_ptr(), self.num_pages, self.page_size, self.kv_heads,
+                                   self.head_dim, k.stride(0), k.stride(1), k.stride(2), _dtype_code(k))
+        self._ref = ctypes.addressof(self.desc)
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
+        k = torch.empty(num_pages, kv_heads, page_size, head_dim, dtype=dtype, device=device)
+        return KVCache(k, torch.empty_like(k))
+
+
+class KVBatch:
+    """A step's batch (see qlora_kv_batch in qlora.h): int32 arrays that
+    qlora_kv_plan fills.  Arrays that are not given are made, on the device
+    of those that are (or `device`)."""
+
+    def __init__(self, batch: int, max_pages: int, tokens: int, max_q_len: int = 0, block_table=None, cu_q=None,
+                 kv_len=None, positions=None, slots=None, device=None):
+        given = [t for t in (block_table, cu_q, kv_len, positions, slots) if t is not None]
+        if device is None:
+            device = given[0].device if given else "cuda"
+        self.device = device = torch.empty(0, device=device).device
+        shapes = {"block_table": (batch, max_pages), "cu_q": (batch + 1,), "kv_len": (batch,), "positions": (tokens,),
+                  "slots": (tokens,)}
+        fill = {"block_table": -1, "positions": -1, "slots": -1}
+        ptrs = []
+        for (name, shape), t in zip(shapes.items(), (block_table, cu_q, kv_len, positions, slots)):
+            if t is None:
+                t = torch.full(shape, fill.get(name, 0), dtype=torch.int32, device=device)
+            ptrs.append(_is(t, torch.int32, shape, device, name))
+            setattr(self, name, t)
+        self.batch, self.max_pages, self.tokens, self.max_q_len = batch, max_pages, tokens, max_q_len
+        self.desc = qlora_kv_batch(batch, max_pages, tokens, max_q_len, *ptrs)
+        self._ref = ctypes.addressof(self.desc)
+
+
+def qlora_build_rope(head_dim: int, base: float = 10000.0) -> qlora_rope:
+    out = qlora_rope()
+    _check(lib.qlora_build_rope(head_dim, base, ctypes.addressof(out)), "qlora_build_rope")
+    return out
+
+
+def qlora_kv_plan(kv: KVBatch, page_size: int, num_pages: int, ctx_len, q_len, free_pages, free_count,
+                  free_count_out=None, stream=None):
+    """free_count_out: free_count itself (updated in place) if not given."""
+    i32, dev = torch.int32, kv.device
+    one = (1,)
+    out = free_count if free_count_out is None else free_count_out
+    args = (kv._ref, page_size, num_pages, _is(ctx_len, i32, (kv.batch,), dev, "ctx_len"),
+            _is(q_len, i32, (kv.batch,), dev, "q_len"), _is(free_pages, i32, (num_pages,), dev, "free_pages"),
+            _is(free_count, i32, one, dev, "free_count"), _is(out, i32, one, dev, "free_count_out"))
+    with _On(dev, stream) as s:
+        _check(lib.qlora_kv_plan(*args, s), "qlora_kv_plan")
+
+
+def qlora_kv_append(cache: KVCache, kv: KVBatch, rope, q, k, v, q_out=None, stream=None):
+    """q [tokens, heads, head_dim], k and v [tokens, kv_heads, head_dim]; q_out: q itself if not given."""
+    _need(q.dim() == 3, "q: need [tokens, heads, head_dim]")
+    _need(cache.device == kv.device, "cache and batch on different devices")
+    T, H, D, dt, dev = kv.tokens, q.shape[1], cache.head_dim, cache.dtype, cache.device
+    new = (T, cache.kv_heads, D)
+    qp = _is(q, dt, (T, H, D), dev, "q")
+    args = (cache._ref, kv._ref, None if rope is None else ctypes.addressof(rope), qp, _is(k, dt, new, dev, "k"),
+            _is(v, dt, new, dev, "v"), H, qp if q_out is None else _is(q_out, dt, (T, H, D), dev, "q_out"))
+    with _On(dev, stream) as s:
+        _check(lib.qlora_kv_append(*args, s), "qlora_kv_append")
+
+
+def qlora_paged_attn_workspace_bytes(cache: KVCache, kv: KVBatch, heads: int) -> int:
+    with _On(cache.device, None):
+        n = lib.qlora_paged_attn_workspace_bytes(cache._ref, kv._ref, heads)
+    _need(n > 0, "not a valid cache, batch and head count")
+    return n
+
+
+def qlora_paged_attn_fwd(cache: KVCache, kv: KVBatch, q, out, scale: float, workspace, window: int = 0, sinks: int = 0,
+                         lse=None, stream=None):
+    """q and out [tokens, heads, head_dim]; lse: float32 [tokens, heads] or None."""
+    _need(q.dim() == 3, "q: need [tokens, heads, head_dim]")
+    _need(cache.device == kv.device and workspace.device == kv.device, "cache, batch and workspace on different devices")
+    _need(workspace.is_contiguous(), "workspace: need a contiguous tensor")
+    T, H, dt, dev = kv.tokens, q.shape[1], cache.dtype, cache.device
+    shape = (T, H, cache.head_dim)
+    qp, op = _is(q, dt, shape, dev, "q"), _is(out, dt, shape, dev, "out")
+    _need(qp != op, "out may not be q")
+    args = (cache._ref, kv._ref, qp, H, scale, window, sinks, op,
+            None if lse is None else _is(lse, torch.float32, (T, H), dev, "lse"), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    with _On(dev, stream) as s:
+        _check(lib.qlora_paged_attn_fwd(*args, s), "qlora_paged_attn_fwd")

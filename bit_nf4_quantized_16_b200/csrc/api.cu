@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "debug.cuh"
+#include "serve.cuh"
 
 namespace qlora {
 
@@ -73,6 +74,18 @@ qlora_status make_map(CUtensorMap *m, CUtensorMapDataType dt, const void *base, 
     cuuint32_t box[2] = {box_inner, box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+qlora_status make_map_4d(CUtensorMap *m, CUtensorMapDataType dt, const void *base, const uint64_t dims[4],
+                         const uint64_t strides[3], const uint32_t box[4], CUtensorMapSwizzle sw)
+{
+    auto fn = encode_fn();
+    if (!fn) return QLORA_ERR_CUDA;
+    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, st[3] = {strides[0], strides[1], strides[2]};
+    const cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]}, estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(m, dt, 4, const_cast<void *>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? QLORA_OK : QLORA_ERR_CUDA;
 }

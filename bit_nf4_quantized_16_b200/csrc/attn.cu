@@ -1,0 +1,177 @@
+// Attention of new tokens over a paged key/value cache: the entry point, the
+// choice of kernel and the kernel that joins split items.  See attn_common.cuh
+// for the schedule, attn_decode.cuh for the kernel of few rows.
+#include <math.h>
+
+#include <algorithm>
+
+#include "attn_decode.cuh"
+#include "common.cuh"
+#include "serve.cuh"
+
+namespace qlora {
+namespace attn {
+
+// Joins the parts of one split item (block x: the CTA that begins it; block y:
+// eight of its rows).  One to eight warps share a row, each taking every
+// n-th part; parts are weighted by 2^(m_i - M) and summed in a fixed order.
+template <int ROWS, int DP, bool F16>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams p)
+{
+    constexpr int V = DP / 32;   // columns per lane
+    __shared__ float acc[8][DP];
+    __shared__ float sum[8];
+    sm100::pdl_wait();
+    sm100::pdl_trigger();
+    const BatchView &v = p.v;
+    const Desc d = p.desc[blockIdx.x];
+    if (d.parts == 0) return;
+    const Request r = load_request(v, d.b);
+    const int row0 = blockIdx.y * 8;
+    const int rows = min(min(r.qn * v.group - d.rt * ROWS, ROWS) - row0, 8);
+    if (rows <= 0) return;
+    const int rp = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8, share = 8 / rp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = warp % rp, sp = warp / rp;
+    constexpr int64_t kSlot = (int64_t)ROWS * DP + 2 * ROWS;
+    auto slot = [&](int i) { return p.part + (i == 0 ? d.first_slot : 2 * (d.cta + i)) * kSlot; };
+    float M = -INFINITY, L = 0.0f;
+    float a[V];
+#pragma unroll
+    for (int k = 0; k < V; k++) a[k] = 0.0f;
+    if (row < rows) {
+        for (int i = lane; i < d.parts; i += 32) M = fmaxf(M, slot(i)[ROWS * DP + row0 + row]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 4
+        for (int i = sp; i < d.parts; i += share) {
+            const float *s = slot(i);
+            const float m = s[ROWS * DP + row0 + row];
+            const float f = m == -INFINITY ? 0.0f : exp2f(m - M);
+            L += f * s[ROWS * DP + ROWS + row0 + row];
+            const float *x = s + (row0 + row) * DP + lane * V;
+#pragma unroll
+            for (int k = 0; k < V; k++) a[k] += f * x[k];
+        }
+    }
+    if (share > 1) {
+#pragma unroll
+        for (int k = 0; k < V; k++) acc[warp][lane * V + k] = a[k];
+        if (lane == 0) sum[warp] = L;
+        __syncthreads();
+        if (sp > 0) return;
+        for (int w = warp + rp; w < 8; w += rp) {
+            L += sum[w];
+#pragma unroll
+            for (int k = 0; k < V; k++) a[k] += acc[w][lane * V + k];
+        }
+    }
+    if (row >= rows) return;
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const int g = d.rt * ROWS + row0 + row;
+    const int64_t orow = (int64_t)(r.q0 + g / v.group) * v.heads + d.h * v.group + g % v.group;
+    const int64_t at = orow * v.head_dim + lane * V;
+    if (lane * V < v.head_dim && QLORA_IN(at + V - 1, (int64_t)v.tokens * v.heads * v.head_dim)) {
+        uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + at);
+#pragma unroll
+        for (int k = 0; k < V / 2; k++) o[k] = pack2<F16>(a[2 * k] * inv, a[2 * k + 1] * inv);
+    }
+    if (lane == 0 && p.lse) p.lse[orow] = L > 0.0f ? (M + log2f(L)) * 0.69314718056f : -INFINITY;
+}
+
+namespace {
+
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+// CTAs of the kernel for few rows: two per SM.
+int decode_grid(const DeviceInfo &d) { return 2 * d.sms; }
+
+size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int DP, bool F16>
+qlora_status launch_decode(AttnParams &p, const DeviceInfo &dev, cudaStream_t s)
+{
+    using C = DecodeCfg<DP>;
+    static PerDeviceOnce once;
+    QLORA_TRY(once.run(dev.device, [] {
+        QLORA_CUDA_TRY(cudaFuncSetAttribute(decode_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            C::kBytes));
+        return QLORA_OK;
+    }));
+    const int grid = decode_grid(dev);
+    {
+        LaunchScope ls(QLORA_KERNEL_ATTENTION, s);
+        QLORA_CUDA_TRY(launch_pdl(decode_kernel<DP, F16>, dim3(grid), dim3(C::kThreads), C::kBytes, s, p));
+    }
+    if (!p.whole_items) {
+        LaunchScope ls(QLORA_KERNEL_ATTENTION, s);
+        QLORA_CUDA_TRY(launch_pdl(combine_kernel<C::kRows, DP, F16>, dim3(grid, C::kRows / 8), dim3(256), 0, s, p));
+    }
+    return launch_status();
+}
+
+qlora_status check_attn(const qlora_kv_cache *c, const qlora_kv_batch *kv, int32_t heads)
+{
+    QLORA_TRY(check_cache(c));
+    QLORA_TRY(check_batch(kv));
+    if (heads < 1 || heads > kMaxHeads || heads % c->kv_heads) return QLORA_ERR_SHAPE;
+    if ((int64_t)kv->max_pages * c->page_size > kMaxPositions || (int64_t)kv->tokens * heads > kMaxPositions)
+        return QLORA_ERR_SHAPE;
+    return QLORA_OK;
+}
+
+size_t workspace_bytes_for(const qlora_kv_cache *c, const DeviceInfo &dev)
+{
+    const int dp = c->head_dim <= 64 ? 64 : 128;
+    const size_t slot = (size_t)(dp == 64 ? DecodeCfg<64>::kSlotFloats : DecodeCfg<128>::kSlotFloats) * 4;
+    return round_up(decode_grid(dev) * sizeof(Desc)) + round_up(2 * (size_t)decode_grid(dev) * slot);
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace qlora
+
+using namespace qlora;
+using namespace qlora::attn;
+
+extern "C" size_t qlora_paged_attn_workspace_bytes(const qlora_kv_cache *cache, const qlora_kv_batch *kv, int32_t heads)
+{
+    DeviceInfo dev;
+    if (check_attn(cache, kv, heads) != QLORA_OK || device_info(&dev) != QLORA_OK) return 0;
+    return workspace_bytes_for(cache, dev);
+}
+
+extern "C" qlora_status qlora_paged_attn_fwd(const qlora_kv_cache *cache, const qlora_kv_batch *kv, const void *q,
+                                             int32_t heads, float scale, int32_t window, int32_t sinks, void *out,
+                                             float *lse, void *workspace, size_t workspace_bytes, void *stream)
+{
+    QLORA_TRY(check_attn(cache, kv, heads));
+    if (!q || !out || !workspace || !kv->block_table || !kv->cu_q || !kv->kv_len) return QLORA_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !isfinite(scale) || window < 0 || sinks < 0) return QLORA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || (lse && !aligned16(lse)) || !aligned16(workspace) ||
+        !aligned16(kv->block_table) || !aligned16(kv->cu_q) || !aligned16(kv->kv_len))
+        return QLORA_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    QLORA_TRY(device_info(&dev));
+    if (workspace_bytes < workspace_bytes_for(cache, dev)) return QLORA_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    AttnParams p{};
+    QLORA_TRY(make_cache_map(&p.tk, cache, cache->k, 16));
+    QLORA_TRY(make_cache_map(&p.tv, cache, cache->v, 16));
+    p.v = BatchView{kv->cu_q, kv->kv_len, kv->block_table, kv->batch, kv->max_pages, kv->tokens, cache->num_pages,
+                    page_shift(cache->page_size), heads, cache->kv_heads, heads / cache->kv_heads, cache->head_dim,
+                    window >= kMaxPositions ? 0 : window, std::min(sinks, (int32_t)kMaxPositions)};
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.desc = static_cast<Desc *>(workspace);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up(decode_grid(dev) * sizeof(Desc)));
+    p.scale_log2 = scale * 1.44269504089f;
+    p.err = device_error_word();
+    if (!p.err) return QLORA_ERR_CUDA;
+    p.timeout_ns = kTimeoutNs;
+    const bool f16 = cache->dtype == QLORA_FP16;
+    if (cache->head_dim <= 64)
+        return f16 ? launch_decode<64, true>(p, dev, s) : launch_decode<64, false>(p, dev, s);
+    return f16 ? launch_decode<128, true>(p, dev, s) : launch_decode<128, false>(p, dev, s);
+}

@@ -1,0 +1,450 @@
+// The step of a served model around its attention: the plan (block tables,
+// slots and positions from the requests' lengths, built on the GPU) and the
+// append of rotated keys and values to the paged cache.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "debug.cuh"
+#include "serve.cuh"
+#include "sm100.cuh"
+
+namespace qlora {
+namespace {
+
+// ---- plan ---------------------------------------------------------------------------
+//
+// One cluster of CTAs.  Every CTA scans all requests (three prefix sums: rows,
+// pages returned, pages taken), so that any of them can answer for any page or
+// token with a binary search in its shared memory; then the CTAs divide the
+// outputs.  Page j of the pool is free_pages[j] below the old count and a page
+// of an ended request above it, read from that request's row of the table,
+// which this call does not change: no CTA reads what another one writes.  Only
+// the count may be updated in place: it is read before the cluster's barrier
+// and written after it.
+//
+// The call moves a few hundred KB at most; what bounds it is latency (one
+// launch, two dependent reads, three scans).
+
+constexpr int kPlanThreads = 512;
+
+struct PlanParams {
+    const int32_t *ctx, *qlen;
+    int32_t *free_pages;
+    const int32_t *free_count;
+    int32_t *free_count_out;
+    int32_t *table, *cu_q, *kv_len, *positions, *slots;
+    int batch, max_pages, tokens, num_pages, page_shift;
+};
+
+// Exclusive prefix of one value per thread over the block, and the total.
+__device__ __forceinline__ int64_t block_scan(int64_t mine, int64_t *warp_sum, int64_t &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+    for (int w = 0; w < kPlanThreads / 32; w++) {
+        const int64_t s = warp_sum[w];
+        if (w < warp) before += s;
+        total += s;
+    }
+    return before + incl - mine;
+}
+
+// The index i with pre[i] <= x < pre[i + 1] (pre ascending, pre[0] <= x < pre[n]).
+__device__ __forceinline__ int owner_of(const int32_t *pre, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int32_t clamp31(int64_t x) { return (int32_t)min(x, (int64_t)INT32_MAX); }
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
+{
+    extern __shared__ int32_t plan_smem[];
+    __shared__ int64_t warp_sum[kPlanThreads / 32];
+    const int n = p.batch, tid = threadIdx.x;
+    int32_t *rows_pre = plan_smem;             // [n + 1] rows before request i, at most `tokens`
+    int32_t *back_pre = rows_pre + n + 1;      // pages returned before i
+    int32_t *take_pre = back_pre + n + 1;      // pages asked for before i
+    const int rank = (int)sm100::cluster_ctarank(), ctas = (int)sm100::cluster_nctarank();
+    const int64_t step = (int64_t)ctas * kPlanThreads, first = (int64_t)rank * kPlanThreads + tid;
+    sm100::pdl_wait();
+    sm100::pdl_trigger();
+    const int page = 1 << p.page_shift;
+    const int count = min(max(*p.free_count, 0), p.num_pages);
+    auto pages = [&](int64_t t) { return (t + page - 1) >> p.page_shift; };
+    const int64_t capacity = (int64_t)p.max_pages << p.page_shift;
+
+    int64_t rows_at = 0, back_at = 0, take_at = 0;
+    for (int b0 = 0; b0 < n; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        const int64_t ctx = b < n ? p.ctx[b] : 0, q = b < n ? p.qlen[b] : 0;
+        const int64_t rows = max(q, (int64_t)0);
+        const int64_t back = q < 0 ? min(pages(max(ctx, (int64_t)0)), (int64_t)p.max_pages) : 0;
+        int64_t total;
+        const int64_t rows0 = rows_at + block_scan(rows, warp_sum, total);
+        rows_at += total;
+        const int64_t back0 = back_at + block_scan(back, warp_sum, total);
+        back_at += total;
+        const bool fits = q >= 0 && ctx >= 0 && ctx + rows <= capacity && rows0 + rows <= p.tokens;
+        const int64_t take = fits ? pages(ctx + rows) - pages(ctx) : 0;
+        const int64_t take0 = take_at + block_scan(take, warp_sum, total);
+        take_at += total;
+        if (b < n) {
+            rows_pre[b] = (int32_t)min(rows0, (int64_t)p.tokens);
+            back_pre[b] = clamp31(back0);
+            take_pre[b] = clamp31(take0);
+        }
+    }
+    if (tid == 0) {
+        rows_pre[n] = (int32_t)min(rows_at, (int64_t)p.tokens);
+        back_pre[n] = clamp31(back_at);
+        take_pre[n] = clamp31(take_at);
+    }
+    __syncthreads();
+    // a valid call returns no more pages than are not in the pool
+    const int pool = (int)min((int64_t)count + back_at, (int64_t)p.num_pages);
+    const int returned = pool - count;
+    // requests take pages in order, and none after the first that the pool cannot serve
+    int lo = 0, hi = n + 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (take_pre[mid] <= pool) lo = mid; else hi = mid;
+    }
+    const int used = take_pre[lo];
+    auto pool_page = [&](int j) -> int32_t {
+        if (j < count) return p.free_pages[j];
+        const int r = j - count, b = owner_of(back_pre, n, r);
+        const int64_t at = (int64_t)b * p.max_pages + r - back_pre[b];
+        return QLORA_IN(at, (int64_t)n * p.max_pages) ? p.table[at] : -1;
+    };
+    auto granted = [&](int b, int64_t ctx, int64_t q) {
+        const int64_t rows = max(q, (int64_t)0);
+        if (q < 0 || ctx < 0 || ctx + rows > capacity || rows_pre[b] + rows > p.tokens) return false;
+        return pages(ctx + rows) == pages(ctx) || take_pre[b + 1] <= pool;
+    };
+
+    for (int64_t b = first; b <= n; b += step) {
+        p.cu_q[b] = rows_pre[b];
+        if (b == n) break;
+        const int64_t ctx = p.ctx[b], q = p.qlen[b];
+        p.kv_len[b] = granted((int)b, ctx, q) ? (int32_t)(ctx + q) : 0;
+    }
+    for (int64_t r = first; r < returned; r += step)
+        if (QLORA_IN(count + r, p.num_pages)) p.free_pages[count + r] = pool_page((int)(count + r));
+    for (int64_t u = first; u < used; u += step) {
+        const int b = owner_of(take_pre, n, (int)u);
+        const int64_t at = (int64_t)b * p.max_pages + pages(p.ctx[b]) + u - take_pre[b];
+        if (QLORA_IN(at, (int64_t)n * p.max_pages)) p.table[at] = pool_page(pool - 1 - (int)u);
+    }
+    const int all_rows = rows_pre[n];
+    for (int64_t t = first; t < p.tokens; t += step) {
+        int32_t pos = -1, slot = -1;
+        if (t < all_rows) {
+            const int b = owner_of(rows_pre, n, (int)t);
+            const int64_t ctx = p.ctx[b];
+            if (granted(b, ctx, p.qlen[b])) {
+                pos = (int32_t)(ctx + t - rows_pre[b]);
+                const int held = (int)pages(ctx), i = pos >> p.page_shift;
+                const int32_t id = i < held ? p.table[(int64_t)b * p.max_pages + i]
+                                            : pool_page(pool - 1 - (take_pre[b] + i - held));
+                if ((unsigned)id < (unsigned)p.num_pages) slot = (id << p.page_shift) + (pos & (page - 1));
+            }
+        }
+        p.positions[t] = pos;
+        p.slots[t] = slot;
+    }
+    // every CTA has read the count
+    if (ctas > 1) sm100::cluster_sync(); else __syncthreads();
+    if (rank == 0 && tid == 0) *p.free_count_out = pool - used;
+}
+
+// ---- append -------------------------------------------------------------------------
+//
+// Pairs (i, i + D/2) of each head rotate by position * base^(-2i/D).  The angle
+// is formed in turns: position times turns per position in binary64, of
+// which the whole part is dropped before anything is rounded to binary32, so
+// that far positions lose nothing (in binary32 the angle of position 130000 is
+// off by up to 2^-7 radians).  The sine and cosine of the rest come from the
+// fast intrinsics on an argument in [-pi, pi], whose absolute error (2^-21) is
+// far below half a step of the 16-bit results.
+//
+// A block takes kTok tokens: it forms their angles once in shared memory, then
+// its threads move 16-byte pieces (a low and a high one that rotate together)
+// of q, k and v.  Bound by memory: every value is read and written once.
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendTokens = 8;   // at most, per block
+
+struct AppendParams {
+    const uint16_t *q, *k, *v;
+    uint16_t *q_out, *kc, *vc;
+    const int32_t *positions, *slots;
+    int64_t stride_page, stride_head, stride_token;
+    int tokens, heads, kv_heads, head_dim, page_shift, num_pages;
+    int block_tokens;
+    int rotate;
+    double turns[64];
+};
+
+template <bool F16>
+__device__ __forceinline__ float2 up2(uint32_t w)
+{
+    if (F16) return __half22float2(*reinterpret_cast<__half2 *>(&w));
+    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&w));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t down2(float a, float b)
+{
+    if (F16) {
+        __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)
+{
+    __shared__ float2 cs[kAppendTokens * 64];
+    __shared__ int32_t slot_of[kAppendTokens];
+    sm100::pdl_wait();
+    sm100::pdl_trigger();
+    const int half = p.head_dim / 2, groups = half / 8;
+    const int64_t t0 = (int64_t)blockIdx.x * p.block_tokens;
+    const int toks = (int)min((int64_t)p.block_tokens, p.tokens - t0);
+    if (threadIdx.x < toks) slot_of[threadIdx.x] = p.slots[t0 + threadIdx.x];
+    if (p.rotate) {
+        for (int e = threadIdx.x; e < toks * half; e += kAppendThreads) {
+            const double turn = (double)p.positions[t0 + e / half] * p.turns[e % half];
+            const float rest = (float)(turn - rint(turn));
+            float s, c;
+            __sincosf(rest * 6.28318530718f, &s, &c);
+            cs[e] = make_float2(c, s);
+        }
+    }
+    __syncthreads();
+    const int per_token = (p.heads + 2 * p.kv_heads) * groups;
+    const int64_t slots = (int64_t)p.num_pages << p.page_shift;
+    for (int e = blockIdx.y * kAppendThreads + threadIdx.x; e < toks * per_token; e += gridDim.y * kAppendThreads) {
+        const int tk = e / per_token, u = e % per_token, head = u / groups, i0 = (u % groups) * 8;
+        const int64_t slot = slot_of[tk], t = t0 + tk;
+        if (slot < 0 || slot >= slots) continue;   // padding, a refused request, or not a place of the cache
+        const uint16_t *src;
+        uint16_t *dst;
+        bool rotate = p.rotate;
+        if (head < p.heads) {
+            const int64_t o = (t * p.heads + head) * p.head_dim;
+            src = p.q + o;
+            dst = p.q_out + o;
+        } else {
+            const bool is_v = head >= p.heads + p.kv_heads;
+            const int h = head - p.heads - (is_v ? p.kv_heads : 0);
+            src = (is_v ? p.v : p.k) + (t * p.kv_heads + h) * p.head_dim;
+            dst = (is_v ? p.vc : p.kc) + (slot >> p.page_shift) * p.stride_page + h * p.stride_head +
+                  (slot & ((1 << p.page_shift) - 1)) * p.stride_token;
+            if (is_v) rotate = false;
+        }
+        uint4 a = *reinterpret_cast<const uint4 *>(src + i0), b = *reinterpret_cast<const uint4 *>(src + i0 + half);
+        if (rotate) {
+            const float2 *tab = cs + tk * half + i0;
+            uint32_t *pa = reinterpret_cast<uint32_t *>(&a), *pb = reinterpret_cast<uint32_t *>(&b);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float2 x = up2<F16>(pa[j]), y = up2<F16>(pb[j]);
+                const float2 c0 = tab[2 * j], c1 = tab[2 * j + 1];
+                pa[j] = down2<F16>(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
+                pb[j] = down2<F16>(x.x * c0.y + y.x * c0.x, x.y * c1.y + y.y * c1.x);
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst + i0) = a;
+        *reinterpret_cast<uint4 *>(dst + i0 + half) = b;
+    }
+}
+
+}  // namespace
+
+qlora_status check_pages(int32_t page_size, int32_t num_pages)
+{
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return QLORA_ERR_SHAPE;
+    if (num_pages < 1 || (int64_t)num_pages * page_size > INT32_MAX) return QLORA_ERR_SHAPE;
+    return QLORA_OK;
+}
+
+qlora_status check_cache(const qlora_kv_cache *c)
+{
+    if (!c || !c->k || !c->v) return QLORA_ERR_INVALID_ARG;
+    if (c->dtype != QLORA_BF16 && c->dtype != QLORA_FP16) return QLORA_ERR_INVALID_ARG;
+    QLORA_TRY(check_pages(c->page_size, c->num_pages));
+    if (c->kv_heads < 1 || c->kv_heads > kMaxHeads) return QLORA_ERR_SHAPE;
+    if (c->head_dim < 16 || c->head_dim > 128 || c->head_dim % 16) return QLORA_ERR_SHAPE;
+    // rows of head_dim values that do not overlap, each on a 16-byte boundary
+    const int64_t st[3] = {c->stride_token, c->stride_head, c->stride_page};
+    const int64_t n[3] = {c->page_size, c->kv_heads, c->num_pages};
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int a, int b) { return st[a] < st[b]; });
+    int64_t reach = c->head_dim;
+    for (int i : order) {
+        if (st[i] % 8 || st[i] < 0 || st[i] >= ((int64_t)1 << 39) / 2) return QLORA_ERR_SHAPE;
+        if (n[i] == 1) continue;
+        if (st[i] < reach) return QLORA_ERR_SHAPE;
+        reach = st[i] * (n[i] - 1) + reach;
+    }
+    if (!aligned16(c->k) || !aligned16(c->v)) return QLORA_ERR_ALIGNMENT;
+    return QLORA_OK;
+}
+
+qlora_status check_batch(const qlora_kv_batch *kv)
+{
+    if (!kv) return QLORA_ERR_INVALID_ARG;
+    if (kv->batch < 1 || kv->batch > kMaxRequests || kv->max_pages < 1 || kv->tokens < 1 ||
+        kv->tokens > kMaxPositions || kv->max_q_len < 0)
+        return QLORA_ERR_SHAPE;
+    return QLORA_OK;
+}
+
+qlora_status make_cache_map(CUtensorMap *m, const qlora_kv_cache *c, const void *base, uint32_t rows)
+{
+    const uint64_t dims[4] = {(uint64_t)c->head_dim, (uint64_t)c->page_size, (uint64_t)c->kv_heads,
+                              (uint64_t)c->num_pages};
+    // a dimension of one element may have any stride; the encoder wants a multiple of 16 bytes above 0
+    auto bytes = [](int64_t stride, int64_t n) { return n == 1 ? (uint64_t)256 : (uint64_t)stride * 2; };
+    const uint64_t strides[3] = {bytes(c->stride_token, c->page_size), bytes(c->stride_head, c->kv_heads),
+                                 bytes(c->stride_page, c->num_pages)};
+    const uint32_t box[4] = {64, rows, 1, 1};
+    return make_map_4d(m, c->dtype == QLORA_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace qlora
+
+using namespace qlora;
+
+extern "C" qlora_status qlora_build_rope(int32_t head_dim, double base, qlora_rope *out)
+{
+    if (!out) return QLORA_ERR_INVALID_ARG;
+    if (head_dim < 16 || head_dim > 128 || head_dim % 16) return QLORA_ERR_SHAPE;
+    if (!(base > 1.0) || !isfinite(base)) return QLORA_ERR_INVALID_ARG;
+    out->head_dim = head_dim;
+    for (int i = 0; i < 64; i++)
+        out->turns[i] = i < head_dim / 2 ? pow(base, -2.0 * i / head_dim) / 6.283185307179586476925 : 0.0;
+    return QLORA_OK;
+}
+
+extern "C" qlora_status qlora_kv_plan(const qlora_kv_batch *kv, int32_t page_size, int32_t num_pages,
+                                      const int32_t *ctx_len, const int32_t *q_len, int32_t *free_pages,
+                                      const int32_t *free_count, int32_t *free_count_out, void *stream)
+{
+    QLORA_TRY(check_batch(kv));
+    QLORA_TRY(check_pages(page_size, num_pages));
+    if (!ctx_len || !q_len || !free_pages || !free_count || !free_count_out || !kv->block_table || !kv->cu_q ||
+        !kv->kv_len || !kv->positions || !kv->slots)
+        return QLORA_ERR_INVALID_ARG;
+    if ((int64_t)kv->max_pages * page_size > kMaxPositions) return QLORA_ERR_SHAPE;
+    const void *all[] = {ctx_len, q_len, free_pages, free_count, free_count_out, kv->block_table, kv->cu_q, kv->kv_len,
+                         kv->positions, kv->slots};
+    for (const void *a : all)
+        if (!aligned16(a)) return QLORA_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    QLORA_TRY(device_info(&dev));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    PlanParams p{ctx_len, q_len, free_pages, free_count, free_count_out, kv->block_table, kv->cu_q, kv->kv_len,
+                 kv->positions, kv->slots, kv->batch, kv->max_pages, kv->tokens, num_pages, page_shift(page_size)};
+    const size_t smem = 3 * ((size_t)kv->batch + 1) * 4;   // at most 49,164 bytes
+    static PerDeviceOnce once;
+    QLORA_TRY(once.run(dev.device, [] {
+        QLORA_CUDA_TRY(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            3 * (kMaxRequests + 1) * 4));
+        return QLORA_OK;
+    }));
+    cudaLaunchConfig_t cfg{};
+    const int ctas = kv->tokens <= 2 * kPlanThreads ? 1 : 8;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)ctas, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    {
+        LaunchScope ls(QLORA_KERNEL_BLOCK, s);
+        QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, plan_kernel, p));
+    }
+    return launch_status();
+}
+
+extern "C" qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora_kv_batch *kv, const qlora_rope *rope,
+                                        const void *q, const void *k, const void *v, int32_t heads, void *q_out,
+                                        void *stream)
+{
+    QLORA_TRY(check_cache(cache));
+    QLORA_TRY(check_batch(kv));
+    if (heads < 1 || heads > kMaxHeads || heads % cache->kv_heads) return QLORA_ERR_SHAPE;
+    if (rope && rope->head_dim != cache->head_dim) return QLORA_ERR_SHAPE;
+    if (!q || !k || !v || !q_out || !kv->slots || (rope && !kv->positions)) return QLORA_ERR_INVALID_ARG;
+    const void *all[] = {q, k, v, q_out, kv->slots, kv->positions};
+    for (const void *a : all)
+        if (!aligned16(a)) return QLORA_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    QLORA_TRY(device_info(&dev));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    AppendParams p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.kc = static_cast<uint16_t *>(cache->k);
+    p.vc = static_cast<uint16_t *>(cache->v);
+    p.positions = kv->positions;
+    p.slots = kv->slots;
+    p.stride_page = cache->stride_page;
+    p.stride_head = cache->stride_head;
+    p.stride_token = cache->stride_token;
+    p.tokens = kv->tokens;
+    p.heads = heads;
+    p.kv_heads = cache->kv_heads;
+    p.head_dim = cache->head_dim;
+    p.page_shift = page_shift(cache->page_size);
+    p.num_pages = cache->num_pages;
+    p.rotate = rope ? 1 : 0;
+    if (rope)
+        for (int i = 0; i < 64; i++) p.turns[i] = rope->turns[i];
+    // as many tokens per block as leave two blocks for every SM; with few tokens, several blocks per token
+    const int pieces = (heads + 2 * cache->kv_heads) * (cache->head_dim / 16);
+    p.block_tokens = std::max(1, std::min(kAppendTokens, kv->tokens / (2 * dev.sms)));
+    const int blocks = (kv->tokens + p.block_tokens - 1) / p.block_tokens;
+    int split = std::max(1, 2 * dev.sms / blocks);
+    split = std::min(split, (p.block_tokens * pieces + kAppendThreads - 1) / kAppendThreads);
+    {
+        LaunchScope ls(QLORA_KERNEL_BLOCK, s);
+        const dim3 grid((unsigned)blocks, (unsigned)split);
+        if (cache->dtype == QLORA_FP16)
+            QLORA_CUDA_TRY(launch_pdl(append_kernel<true>, grid, dim3(kAppendThreads), 0, s, p));
+        else
+            QLORA_CUDA_TRY(launch_pdl(append_kernel<false>, grid, dim3(kAppendThreads), 0, s, p));
+    }
+    return launch_status();
+}

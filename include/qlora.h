@@ -503,6 +503,149 @@ QLORA_API qlora_status qlora_linear_adapter_bwd(const qlora_nf4_weight *w, const
                                                 const float *H_saved, void *workspace, size_t workspace_bytes,
                                                 void *stream, const qlora_linear_opts *opts);
 
+/*
+ * ---- Serving: a paged key/value cache and the attention that reads it ----
+ *
+ * The pages finetune adapters and do not describe how the model is then
+ * served; these entry points are the serving form of the block's attention.
+ * One step of a served model processes new tokens of many requests at once:
+ * a whole prompt, a chunk of one, or a single token each.
+ *   1. qlora_kv_plan     gives every request the pages that its new tokens
+ *                        need, and every new token its position and its place;
+ *   2. per layer: qlora_kv_append rotates q and k and writes k and v to the
+ *      layer's cache; qlora_paged_attn_fwd attends over it.
+ * Nothing reads a length on the host, so a step of fixed `tokens` and `batch`
+ * can be captured into a CUDA graph and replayed with other lengths.
+ * These are forward operators (a cache has no gradient); the training form
+ * is qlora_block_bwd.
+ *
+ * A layer's cache.  k and v hold position s of page p of head h at
+ *   p * stride_page + h * stride_head + s * stride_token    (elements)
+ * with head_dim contiguous values; both orders of heads and positions are
+ * served.  page_size: a power of two, 16 to 256.  num_pages * page_size <=
+ * 2^31 - 1.  head_dim: a multiple of 16, 16 to 128.  Strides: multiples of 8,
+ * such that no two rows overlap.  dtype: QLORA_BF16 or QLORA_FP16, also the type of q,
+ * k, v and the output.  Pages need not be initialized: what lies at or
+ * beyond a request's length is never used, whatever it holds.
+ */
+typedef struct {
+    void *k, *v; /* device */
+    int32_t num_pages, page_size, kv_heads, head_dim;
+    int64_t stride_page, stride_head, stride_token;
+    qlora_dtype dtype;
+} qlora_kv_cache;
+
+/*
+ * A step's batch: sizes known on the host and arrays on the device.
+ *   batch       requests, 1 to 4096.
+ *   max_pages   width of the block table; max_pages * page_size <= 2^30.
+ *   tokens      rows of q, k, v and the output (capacity: the requests' new
+ *               tokens are packed from row 0, the rest is padding).
+ *   max_q_len   no request has more new tokens than this; 0: not known.  It
+ *               only steers which kernel is used, results do not depend on it
+ *               beyond their rounding.
+ *   block_table [batch][max_pages] page ids, request by request.
+ *   cu_q        [batch + 1] first row of each request, and the rows' end.
+ *   kv_len      [batch] positions of each request, its new tokens included.
+ *   positions   [tokens] position of each row in its request; -1: none.
+ *   slots       [tokens] page * page_size + offset of each row; -1: none.
+ * qlora_kv_plan writes all five (block_table: the new entries); a caller with
+ * an allocator of its own may fill them itself.  qlora_kv_append reads positions and
+ * slots, qlora_paged_attn_fwd the other three; arrays that a call does not
+ * use may be NULL.
+ */
+typedef struct {
+    int32_t batch, max_pages, tokens, max_q_len;
+    int32_t *block_table, *cu_q, *kv_len, *positions, *slots; /* device */
+} qlora_kv_batch;
+
+/*
+ * qlora_kv_plan -- block tables, slots and positions from the requests'
+ * lengths, built on the GPU.
+ *   ctx_len     device [batch], positions that request b holds already; its
+ *               first ceil(ctx_len / page_size) table entries are its pages.
+ *   q_len       device [batch], its new tokens (0: none this step); negative: the
+ *               request has ended and its pages go back to the pool.
+ *   free_pages  device [num_pages], the pool: a stack whose first
+ *               *free_count entries are free page ids.  Returned pages are
+ *               pushed (in the requests' order), then new pages are taken from
+ *               the top: first request first, lowest position first.
+ *   free_count, free_count_out  device, 1 value each: before and after; may be
+ *               the same address.
+ * A request is refused if its positions do not fit its table row, its rows do not fit
+ * `tokens`, its ctx_len is negative, or the pool cannot serve it; after the
+ * first that the pool cannot serve, no other gets new pages in this call.  A
+ * refused request keeps its pages, gets none, kv_len 0, and position and slot -1
+ * for its rows; a later call may serve it.  An ended request's kv_len is 0.
+ * Table entries outside [ceil(ctx_len / page_size), ceil((ctx_len + q_len) /
+ * page_size)) are left as they were.  ctx_len, q_len and the pool are read
+ * only on the device.  No two calls may work on the same pool at once.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA, UNSUPPORTED.
+ */
+QLORA_API qlora_status qlora_kv_plan(const qlora_kv_batch *kv, int32_t page_size, int32_t num_pages,
+                                     const int32_t *ctx_len, const int32_t *q_len, int32_t *free_pages,
+                                     const int32_t *free_count, int32_t *free_count_out, void *stream);
+
+/*
+ * Frequencies of the rotary position embedding: pair i < head_dim / 2 turns by
+ * base^(-2 i / head_dim) radians per position; turns[i] holds that divided by
+ * 2 pi.  A caller may scale the entries (position interpolation).
+ * qlora_build_rope: host-only.  head_dim a multiple of 16, 16 to 128; base > 1.
+ * Errors: INVALID_ARG, SHAPE.
+ */
+typedef struct {
+    int32_t head_dim;
+    double turns[64];
+} qlora_rope;
+QLORA_API qlora_status qlora_build_rope(int32_t head_dim, double base, qlora_rope *out);
+
+/*
+ * qlora_kv_append -- rotates q and k by their positions and writes k and v to
+ * the cache.
+ *   rope   NULL: no rotation.  Else pairs (i, i + head_dim / 2) of every head,
+ *          (a, b) -> (a cos - b sin, a sin + b cos), in fp32 from angles formed
+ *          in binary64, rounded once.
+ *   q      device [tokens][heads][head_dim], q_out the same shape; q_out may
+ *          be q (in place).  k, v device [tokens][kv_heads][head_dim].
+ *   heads  a multiple of the cache's kv_heads.
+ * Rows whose slot is -1 or not a place of the cache are skipped: nothing is written
+ * for them, q_out included.  Two rows with the same slot are the caller's error
+ * (either may remain).
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, CUDA, UNSUPPORTED.
+ */
+QLORA_API qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora_kv_batch *kv, const qlora_rope *rope,
+                                       const void *q, const void *k, const void *v, int32_t heads, void *q_out,
+                                       void *stream);
+
+/*
+ * qlora_paged_attn_fwd -- causal attention of the new tokens over the cache.
+ * Row t of request b, at position x = kv_len - (cu_q[b + 1] - cu_q[b]) + t -
+ * cu_q[b], sees position j <= x if window is 0, or j > x - window, or j < sinks:
+ *     out[t][h] = sum_j p_j v_j,  p = softmax over those j of scale * q[t][h] . k_j
+ * with k, v of head h / (heads / kv_heads).  A row that sees nothing gets
+ * zeros.  Positions whose table entry is no page of the cache, or that lie
+ * beyond the table, are left out as if they were masked.  Rows of `out` at
+ * and after cu_q[batch] are left as they were.
+ *   q, out  device [tokens][heads][head_dim] of the cache's type, tokens *
+ *           heads <= 2^30; out may not be q.
+ *   scale   finite, above 0.
+ *   window  0: none; else each row sees its last `window` positions (its own
+ *           among them) and the first `sinks` of the request.
+ *   lse     device float [tokens][heads] or NULL: log sum exp of the scores (-inf for a
+ *           row that sees nothing).
+ *   workspace  device, >= qlora_paged_attn_workspace_bytes, any content;
+ *           calls that overlap in time need one each.
+ * Softmax statistics and sums are fp32.  The division of work depends on the lengths
+ * and the device only: the same call gives the same bits.
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, WORKSPACE, CUDA, UNSUPPORTED; a bounded
+ * wait that gave up is reported by qlora_check_device_error.
+ */
+QLORA_API size_t qlora_paged_attn_workspace_bytes(const qlora_kv_cache *cache, const qlora_kv_batch *kv,
+                                                  int32_t heads);
+QLORA_API qlora_status qlora_paged_attn_fwd(const qlora_kv_cache *cache, const qlora_kv_batch *kv, const void *q,
+                                            int32_t heads, float scale, int32_t window, int32_t sinks, void *out,
+                                            float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 QLORA_API const char *qlora_status_string(qlora_status status);
 
