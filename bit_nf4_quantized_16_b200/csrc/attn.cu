@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "attn_chunk.cuh"
 #include "attn_decode.cuh"
 #include "common.cuh"
 #include "serve.cuh"
@@ -110,6 +111,34 @@ qlora_status launch_decode(AttnParams &p, const DeviceInfo &dev, cudaStream_t s)
     return launch_status();
 }
 
+template <int DP, bool F16>
+qlora_status launch_chunk(AttnParams &p, const DeviceInfo &dev, cudaStream_t s)
+{
+    using C = ChunkCfg<DP>;
+    static PerDeviceOnce once;
+    QLORA_TRY(once.run(dev.device, [] {
+        QLORA_CUDA_TRY(cudaFuncSetAttribute(chunk_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            C::kBytes));
+        return QLORA_OK;
+    }));
+    {
+        LaunchScope ls(QLORA_KERNEL_ATTENTION, s);
+        QLORA_CUDA_TRY(launch_pdl(chunk_kernel<DP, F16>, dim3(dev.sms), dim3(C::kThreads), C::kBytes, s, p));
+    }
+    {
+        LaunchScope ls(QLORA_KERNEL_ATTENTION, s);
+        QLORA_CUDA_TRY(launch_pdl(combine_kernel<C::kRows, DP, F16>, dim3(dev.sms, C::kRows / 8), dim3(256), 0, s, p));
+    }
+    return launch_status();
+}
+
+// More than one tile of 16 rows per key/value head: the kernel of many rows.
+bool many_rows(const qlora_kv_batch *kv, int group)
+{
+    const int64_t q = kv->max_q_len ? std::min(kv->max_q_len, kv->tokens) : kv->tokens;
+    return q * group > 16;
+}
+
 qlora_status check_attn(const qlora_kv_cache *c, const qlora_kv_batch *kv, int32_t heads)
 {
     QLORA_TRY(check_cache(c));
@@ -120,11 +149,13 @@ qlora_status check_attn(const qlora_kv_cache *c, const qlora_kv_batch *kv, int32
     return QLORA_OK;
 }
 
-size_t workspace_bytes_for(const qlora_kv_cache *c, const DeviceInfo &dev)
+size_t workspace_bytes_for(const qlora_kv_cache *c, const qlora_kv_batch *kv, int32_t heads, const DeviceInfo &dev)
 {
-    const int dp = c->head_dim <= 64 ? 64 : 128;
-    const size_t slot = (size_t)(dp == 64 ? DecodeCfg<64>::kSlotFloats : DecodeCfg<128>::kSlotFloats) * 4;
-    return round_up(decode_grid(dev) * sizeof(Desc)) + round_up(2 * (size_t)decode_grid(dev) * slot);
+    const bool wide = c->head_dim > 64, many = many_rows(kv, heads / c->kv_heads);
+    const int grid = many ? dev.sms : decode_grid(dev);
+    const size_t slot = 4 * (size_t)(many ? (wide ? ChunkCfg<128>::kSlotFloats : ChunkCfg<64>::kSlotFloats)
+                                          : (wide ? DecodeCfg<128>::kSlotFloats : DecodeCfg<64>::kSlotFloats));
+    return round_up(decode_grid(dev) * sizeof(Desc)) + round_up(2 * grid * slot);
 }
 
 }  // namespace
@@ -138,7 +169,7 @@ extern "C" size_t qlora_paged_attn_workspace_bytes(const qlora_kv_cache *cache, 
 {
     DeviceInfo dev;
     if (check_attn(cache, kv, heads) != QLORA_OK || device_info(&dev) != QLORA_OK) return 0;
-    return workspace_bytes_for(cache, dev);
+    return workspace_bytes_for(cache, kv, heads, dev);
 }
 
 extern "C" qlora_status qlora_paged_attn_fwd(const qlora_kv_cache *cache, const qlora_kv_batch *kv, const void *q,
@@ -153,11 +184,13 @@ extern "C" qlora_status qlora_paged_attn_fwd(const qlora_kv_cache *cache, const 
         return QLORA_ERR_ALIGNMENT;
     DeviceInfo dev;
     QLORA_TRY(device_info(&dev));
-    if (workspace_bytes < workspace_bytes_for(cache, dev)) return QLORA_ERR_WORKSPACE;
+    if (workspace_bytes < workspace_bytes_for(cache, kv, heads, dev)) return QLORA_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     AttnParams p{};
-    QLORA_TRY(make_cache_map(&p.tk, cache, cache->k, 16));
-    QLORA_TRY(make_cache_map(&p.tv, cache, cache->v, 16));
+    const bool many = many_rows(kv, heads / cache->kv_heads);
+    const uint32_t box = many ? std::min(cache->page_size, 128) : 16;
+    QLORA_TRY(make_cache_map(&p.tk, cache, cache->k, box));
+    QLORA_TRY(make_cache_map(&p.tv, cache, cache->v, box));
     p.v = BatchView{kv->cu_q, kv->kv_len, kv->block_table, kv->batch, kv->max_pages, kv->tokens, cache->num_pages,
                     page_shift(cache->page_size), heads, cache->kv_heads, heads / cache->kv_heads, cache->head_dim,
                     window >= kMaxPositions ? 0 : window, std::min(sinks, (int32_t)kMaxPositions)};
@@ -171,6 +204,11 @@ extern "C" qlora_status qlora_paged_attn_fwd(const qlora_kv_cache *cache, const 
     if (!p.err) return QLORA_ERR_CUDA;
     p.timeout_ns = kTimeoutNs;
     const bool f16 = cache->dtype == QLORA_FP16;
+    if (many) {
+        if (cache->head_dim <= 64)
+            return f16 ? launch_chunk<64, true>(p, dev, s) : launch_chunk<64, false>(p, dev, s);
+        return f16 ? launch_chunk<128, true>(p, dev, s) : launch_chunk<128, false>(p, dev, s);
+    }
     if (cache->head_dim <= 64)
         return f16 ? launch_decode<64, true>(p, dev, s) : launch_decode<64, false>(p, dev, s);
     return f16 ? launch_decode<128, true>(p, dev, s) : launch_decode<128, false>(p, dev, s);

@@ -1,0 +1,599 @@
+// Paged attention for many query rows (chunks and whole prompts): bound by the
+// tensor cores and the exponentials.
+//
+// One CTA per SM, persistent over its items of 256 rows x tiles of 128
+// positions.  The rows form two halves of 128, A and B, whose softmax alternates
+// with the other half's products:
+//   warps 0-3, 4-7  softmax of half A, B: one thread per row
+//   warp 8          the schedule (it hands the items to the other warps through
+//                   a ring in shared memory), and keys and values: a ring of
+//                   tiles filled by TMA page by page
+//   warp 9          issues the products
+//   warps 10, 11    query rows of half A, B
+// Scores S = Q K^T (tcgen05, both operands in shared memory) land in tensor
+// memory; a softmax thread reads its row, and writes the weights as 16-bit
+// values over the scores, where the second product O += P V takes them as its
+// left operand: they never pass through shared memory.  512 columns of
+// tensor memory hold S/P and O of both halves.  The order of issue is
+//   S_A(0) S_B(0) | PV_A(0) S_A(1) PV_B(0) S_B(1) | PV_A(1) ...
+// and runs on across items, so that one half's epilogue overlaps the other's
+// products.  Products of one CTA complete in order: the completion of S(j + 1)
+// tells the softmax that PV(j) is done too.
+//
+// Softmax: one pass, and the output is rescaled only when a row's maximum has
+// grown by more than 2^8 since its last rescaling (weights stay below 2^8, sums
+// and outputs are exact in scale); rescaling is then done by the softmax
+// threads, between S(j) and the weights of j.  The weights are rounded to the
+// operands' 16-bit type (half a step each, averaged over the keys: the output's
+// own rounding is as large); sums are taken of the unrounded fp32 weights.
+#pragma once
+#include "attn_common.cuh"
+
+namespace qlora {
+namespace attn {
+
+template <int DP>
+struct ChunkCfg {
+    static constexpr int kThreads = 384, kRows = 256, kTile = 128, kOv = 1;
+    static constexpr uint32_t kQBytes = 128 * DP * 2;      // one half
+    static constexpr uint32_t kTileBytes = 128 * DP * 2;   // keys or values of one tile
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr uint32_t kRingOff = 2 * kQBytes;
+    static constexpr uint32_t kBarOff = kRingOff + kStages * kTileBytes;
+    static constexpr uint32_t kBytes = kBarOff + 1024 + 1024;   // + alignment slack
+    static constexpr int kSlotFloats = kRows * DP + 2 * kRows;
+    static constexpr uint32_t kOCol = 256;                 // O_A, O_B at 256 + DP * half; S at 128 * half
+    static constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 2 * 208 + 88 = 3 * 168, the launch's share
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// D[tmem] (+)= A[tmem, K-major 16-bit] * B[smem desc]
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One half of an item: its rows' positions, and which of the CTA's tiles it needs.
+struct Half {
+    int rows, first, last;   // valid rows (0: none), position of the first and the last
+    int t_first, t_last;     // first and last tile needed of [t0, t1); t_last < t_first: none
+
+    __device__ __forceinline__ bool needs(const BatchView &v, int tile) const
+    {
+        const int a = tile * 128;
+        return a <= last && (v.window <= 0 || a + 127 > first - v.window || a < v.sinks);
+    }
+    __device__ __forceinline__ bool has() const { return t_last >= t_first; }
+};
+
+__device__ __forceinline__ Half half_of(const BatchView &v, const Item &it, int half)
+{
+    Half f;
+    f.rows = min(max(it.r.qn * v.group - it.rt * 256 - half * 128, 0), 128);
+    f.first = f.last = -1;
+    f.t_first = it.t0;
+    f.t_last = it.t0 - 1;
+    if (f.rows == 0) return f;
+    item_positions<128>(v, it.r, it.rt * 2 + half, f.first, f.last);
+    f.t_last = it.t1 - 1;
+    while (f.t_last >= f.t_first && !f.needs(v, it.tiles.at(f.t_last))) f.t_last--;
+    while (f.t_last >= f.t_first && !f.needs(v, it.tiles.at(f.t_first))) f.t_first++;
+    return f;
+}
+
+// What the schedule hands to the other warps.
+struct ChunkItem {
+    Tiles tiles;
+    int t0, t1;
+    int h;            // key/value head; -1: no more items
+    int q0;           // first row of the request
+    int row0;         // first row of the item: r / group is a token of the request
+    int pos0;         // position of the request's first row
+    int whole, begins;
+    Half half[2];
+    int b, rt, parts;
+};
+
+struct ChunkBars {
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t s_full[2], p_ready[2], o_full[2], q_full[2], q_free[2];
+    uint64_t item_full[4], item_empty[4];
+    uint64_t tail, drain;
+    uint32_t tmem;
+    int abort;
+    uint32_t bad[8];   // per tile (mod 8): bit i, positions 16 i ... + 15 are on no page of the cache
+    ChunkItem item[4];
+};
+
+// Bits 0 ... n - 1 of a word (n of any size).
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// Bounded wait; false after the limit or when another role gave up.
+__device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, ChunkBars *b, const AttnParams &p)
+{
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = sm100::globaltimer_ns();
+    for (uint32_t spin = 0;; spin++) {
+        if (sm100::mbar_try_wait(bar, parity)) return true;
+        if ((spin & 63u) == 63u) {
+            if (*reinterpret_cast<volatile int *>(&b->abort)) return false;
+            if (sm100::globaltimer_ns() - t0 > p.timeout_ns) {
+                atomicExch(p.err, 1);
+                *reinterpret_cast<volatile int *>(&b->abort) = 1;
+                return false;
+            }
+        }
+    }
+}
+
+template <int DP, bool F16>
+__global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ AttnParams p)
+{
+    using C = ChunkCfg<DP>;
+    using W = Walker<C::kThreads, C::kRows, C::kTile, C::kOv>;
+    using namespace sm100;
+    constexpr int ST = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    ChunkBars *bars = reinterpret_cast<ChunkBars *>(smem + C::kBarOff);
+    static_assert(sizeof(ChunkBars) <= 1024, "barriers and items fit their place");
+    int64_t *pre = reinterpret_cast<int64_t *>(smem + C::kRingOff);   // before the ring is used
+    const BatchView &v = p.v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; s++) {
+            mbar_init(&bars->kv_full[s], 1);
+            mbar_init(&bars->kv_empty[s], 1);
+        }
+        for (int h = 0; h < 2; h++) {
+            mbar_init(&bars->s_full[h], 1);
+            mbar_init(&bars->p_ready[h], 4);
+            mbar_init(&bars->o_full[h], 1);
+            mbar_init(&bars->q_full[h], 1);
+            mbar_init(&bars->q_free[h], 1);
+        }
+        for (int i = 0; i < 4; i++) {
+            mbar_init(&bars->item_full[i], 1);
+            mbar_init(&bars->item_empty[i], 11);   // 8 softmax warps, the products, 2 warps of query rows
+        }
+        mbar_init(&bars->tail, 1);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&p.tk);
+        tma_prefetch_desc(&p.tv);
+    }
+    if (warp == 9) {
+        tmem_alloc(&bars->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    pdl_wait();
+    pdl_trigger();
+    schedule_scan<C::kThreads, C::kRows, C::kTile, C::kOv>(v, pre);   // its barriers publish the above
+    tc_fence_after();
+    const int64_t total = pre[C::kThreads];
+    const int64_t G = min((int64_t)gridDim.x, total), cta = blockIdx.x;
+    if (threadIdx.x == 0) p.desc[cta].parts = 0;
+    const uint32_t tmem = bars->tmem;
+    W walk;
+    if (warp == 8) {
+        walk.init(v, pre, cta < G ? cta * total / G : 0, cta < G ? (cta + 1) * total / G : 0, p.whole_items);
+        fence_proxy_async_smem();
+    }
+    __syncthreads();   // the prefix sums have been read: the ring is free
+
+    // The n-th item of this CTA, or null at the end or after a failure.
+    auto item_at = [&](uint32_t n) -> const ChunkItem * {
+        bool ok = chunk_wait(&bars->item_full[n & 3], (n >> 2) & 1, bars, p);
+        if (warp != 9) ok = __all_sync(0xffffffffu, ok);   // the products' warp runs one thread
+        if (!ok) return nullptr;
+        const ChunkItem *it = &bars->item[n & 3];
+        return it->h < 0 ? nullptr : it;
+    };
+    // The row of q, out and lse (times heads, plus the head) of an item's row.
+    auto tensor_row = [&](const ChunkItem *it, int r) {
+        const int g = it->row0 + r;
+        return (int64_t)(it->q0 + g / v.group) * v.heads + it->h * v.group + g % v.group;
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        if (warp == 8) {
+            // ---- schedule; keys and values, in the order K(0) V(0) K(1) V(1) ... ----
+            const int box = min(1 << v.page_shift, 128), pieces = 128 / box;
+            uint32_t n = 0, tiles = 0, tails = 0, items = 0;   // ring entries, tiles, tail waits, items so far
+            bool ok = true, more = true;
+            while (more) {
+                Item it;
+                more = walk.next(v, it);
+                ok = chunk_wait(&bars->item_empty[items & 3], ((items >> 2) & 1) ^ 1, bars, p);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    ChunkItem &o = bars->item[items & 3];
+                    o.h = -1;
+                    if (more) {
+                        o.tiles = it.tiles;
+                        o.t0 = it.t0;
+                        o.t1 = it.t1;
+                        o.h = it.h;
+                        o.q0 = it.r.q0;
+                        o.row0 = it.rt * 256;
+                        o.pos0 = it.r.kv - it.r.qn;
+                        o.whole = it.whole;
+                        o.begins = it.begins;
+                        o.half[0] = half_of(v, it, 0);
+                        o.half[1] = half_of(v, it, 1);
+                        o.b = it.b;
+                        o.rt = it.rt;
+                        o.parts = it.begins ? cta_of_last(it.end, G, total) - (int)cta + 1 : 0;
+                    }
+                    mbar_arrive(&bars->item_full[items & 3]);
+                }
+                items++;
+                if (!more) break;
+                for (int t = it.t0; ok && t < it.t1; t++, tiles++) {
+                    const int tok0 = it.tiles.at(t) * 128, mine = tok0 + lane * box;
+                    int page = v.num_pages;   // a page outside the cache: the copy fills zeros
+                    bool bad = false;
+                    if (lane < pieces && mine < it.r.kv) {
+                        const int id = page_of(v, it.b, mine);
+                        bad = id < 0;
+                        if (id >= 0) page = id;
+                    }
+                    const uint32_t bad_mask = __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, bad, (lane & 7) * 16 / box)) & 0xffu;
+                    const int row = mine & ((1 << v.page_shift) - 1);
+                    for (int kv = 0; kv < 2; kv++, n++) {
+                        const int s = n % ST;
+                        ok = chunk_wait(&bars->kv_empty[s], ((n / ST) & 1) ^ 1, bars, p);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        uint8_t *dst = smem + C::kRingOff + s * C::kTileBytes;
+                        const bool tail = kv == 1 && tok0 + 128 > it.r.kv;
+                        uint64_t *bar = tail ? &bars->tail : &bars->kv_full[s];
+                        if (lane == 0) {
+                            if (kv == 0) bars->bad[tiles & 7] = bad_mask;
+                            mbar_arrive_expect_tx(bar, C::kTileBytes);
+                        }
+                        __syncwarp();
+                        if (lane < pieces) {
+#pragma unroll
+                            for (int c = 0; c < DP / 64; c++)
+                                tma_load_4d(dst + c * 16384 + lane * box * 128, kv ? &p.tv : &p.tk, bar, 64 * c, row, it.h,
+                                            page);
+                        }
+                        if (tail) {
+                            // positions at or beyond the length were never written and may hold
+                            // anything; their weight is 0, but 0 times a NaN is not
+                            ok = chunk_wait(&bars->tail, tails & 1, bars, p);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            tails++;
+                            const int r0 = max(it.r.kv - tok0, 0), r1 = min((r0 + box - 1) / box * box, 128);
+                            for (int i = lane; i < (r1 - r0) * (DP / 8); i += 32) {
+                                const int r = r0 + i / (DP / 8), ch = i % (DP / 8);
+                                *reinterpret_cast<uint4 *>(dst + (ch >> 3) * 16384 + r * 128 + (ch & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars->kv_full[s]);
+                        }
+                    }
+                }
+                if (!ok) break;
+            }
+            if (!ok) {
+                // wait (bounded) for the copies in flight
+                for (uint32_t j = n > (uint32_t)ST ? n - ST : 0; j < n; j++)
+                    mbar_wait_bounded(&bars->kv_full[j % ST], (j / ST) & 1, p.timeout_ns / 8);
+                mbar_wait_bounded(&bars->tail, tails & 1, p.timeout_ns / 8);
+            }
+        } else if (warp == 9) {
+            // ---- products ----
+            if (lane == 0) {
+                const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0, F16), idesc_o = idesc_bf16_f32(128, DP, 0, 1, F16);
+                const uint32_t ring = smem_u32(smem + C::kRingOff), qbase = smem_u32(smem);
+                const int k_steps = v.head_dim / 16;
+                uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // weights and query tiles taken
+                bool ok = true;
+                auto wait = [&](uint64_t *bar, uint32_t parity) {
+                    if (ok) ok = chunk_wait(bar, parity, bars, p);
+                    if (ok) tc_fence_after();
+                };
+                // S runs one tile ahead of PV, across items.  An item is given back before the
+                // next one is waited for: PV keeps a copy of what it needs.
+                const ChunkItem *si = nullptr;   // the item of the next tile of S
+                uint32_t items = 0;              // items begun
+                int st = 0;
+                auto next_tile = [&]() {
+                    st++;
+                    while (!si || st >= si->t1) {
+                        if (si) mbar_arrive(&bars->item_empty[(items - 1) & 3]);
+                        si = item_at(items++);
+                        if (!si) return;
+                        st = si->t0;
+                    }
+                };
+                auto issue_scores = [&](int h, uint32_t slot) {
+                    const Half &f = si->half[h];
+                    if (!f.has() || !f.needs(v, si->tiles.at(st))) return;
+                    if (st == f.t_first) {
+                        wait(&bars->q_full[h], nq[h] & 1);
+                        nq[h]++;
+                    }
+                    if (!ok) return;
+                    for (int kk = 0; kk < k_steps; kk++) {
+                        const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
+                        tc_mma_bf16(tmem + 128 * h, smem_desc_sw128(qbase + h * C::kQBytes + o, 16, 1024),
+                                    smem_desc_sw128(ring + slot * C::kTileBytes + o, 16, 1024), idesc_s, kk > 0);
+                    }
+                    tc_commit(&bars->s_full[h]);
+                    if (st == f.t_last) tc_commit(&bars->q_free[h]);
+                };
+                uint32_t e = 0;   // ring entry of K of the tile of S
+                next_tile();
+                if (si) {
+                    wait(&bars->kv_full[0], 0);
+                    issue_scores(0, 0);
+                    issue_scores(1, 0);
+                    if (ok) tc_commit(&bars->kv_empty[0]);
+                }
+                while (si && ok) {
+                    // PV of this tile, S of the next
+                    const Half pf[2] = {si->half[0], si->half[1]};
+                    const int pt = st, tile = si->tiles.at(st);
+                    const uint32_t ve = (e + 1) % ST, ke = (e + 2) % ST;
+                    next_tile();
+                    bool k_here = false;
+                    wait(&bars->kv_full[ve], ((e + 1) / ST) & 1);
+                    for (int h = 0; h < 2 && ok; h++) {
+                        const Half &f = pf[h];
+                        if (f.has() && f.needs(v, tile)) {
+                            wait(&bars->p_ready[h], np[h] & 1);
+                            np[h]++;
+                            if (!ok) break;
+#pragma unroll
+                            for (int kk = 0; kk < 8; kk++)
+                                tc_mma_ts(tmem + C::kOCol + DP * h, tmem + 128 * h + 8 * kk,
+                                          smem_desc_sw128(ring + ve * C::kTileBytes + 2048 * kk, 16384, 1024), idesc_o,
+                                          pt > f.t_first || kk > 0);
+                            if (pt == f.t_last) tc_commit(&bars->o_full[h]);
+                        }
+                        if (h == 1) tc_commit(&bars->kv_empty[ve]);
+                        if (si) {
+                            if (!k_here) wait(&bars->kv_full[ke], ((e + 2) / ST) & 1);
+                            k_here = true;
+                            if (ok) issue_scores(h, ke);
+                            if (h == 1 && ok) tc_commit(&bars->kv_empty[ke]);
+                        }
+                    }
+                    e += 2;
+                }
+                if (!ok) {
+                    // wait (bounded) until the products already issued finish
+                    tc_commit(&bars->drain);
+                    mbar_wait_bounded(&bars->drain, 0, p.timeout_ns);
+                }
+            }
+        } else {
+            // ---- query rows of one half ----
+            const int h = warp - 10;
+            uint8_t *dst = smem + h * C::kQBytes;
+            uint32_t n = 0, items = 0;
+            bool ok = true;
+            for (const ChunkItem *it; ok && (it = item_at(items)); items++) {
+                const Half f = it->half[h];
+                if (f.has()) {
+                    if (n > 0) ok = chunk_wait(&bars->q_free[h], (n - 1) & 1, bars, p);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+#pragma unroll 4
+                    for (int i = lane; i < 128 * (DP / 8); i += 32) {
+                        const int r = i / (DP / 8), ch = i % (DP / 8);
+                        const bool in = r < f.rows && ch * 8 < v.head_dim;
+                        const int64_t o = in ? tensor_row(it, h * 128 + r) * v.head_dim + ch * 8 : 0;
+                        const bool there = in && QLORA_IN(o + 7, (int64_t)v.tokens * v.heads * v.head_dim);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                         smem_u32(dst + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4))),
+                                     "l"(static_cast<const uint16_t *>(p.q) + o), "r"(there ? 16 : 0)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async_smem();
+                    n++;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (f.has()) mbar_arrive(&bars->q_full[h]);
+                    mbar_arrive(&bars->item_empty[items & 3]);
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+        // ---- softmax and epilogue of one half ----
+        const int h = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t s_addr = tmem + lanes + 128 * h, o_addr = tmem + lanes + C::kOCol + DP * h;
+        uint32_t n_s = 0, n_o = 0, tiles = 0;
+        bool ok = true;
+        const ChunkItem *it;
+        for (uint32_t items = 0; ok && (it = item_at(items)); items++) {
+            const bool valid = row < it->half[h].rows;
+            const int t0 = it->half[h].t_first, t1 = it->half[h].t_last;
+            const bool has = t1 >= t0;
+            const int pos = valid ? it->pos0 + (it->row0 + h * 128 + row) / v.group : -1;
+            float m = -INFINITY, l = 0.0f;   // m: the maximum that the weights are taken against
+            for (int t = it->t0; t < it->t1; t++, tiles++) {
+                const int tile = it->tiles.at(t), tok0 = tile * 128;
+                if (!has || !it->half[h].needs(v, tile)) continue;
+                ok = chunk_wait(&bars->s_full[h], n_s & 1, bars, p);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                n_s++;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; c++) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);
+                tmem_ld_wait();
+                const uint32_t bad = bars->bad[tiles & 7];
+                const bool all_seen = tok0 + 127 <= it->half[h].first && bad == 0 &&
+                                      (v.window <= 0 || tok0 > it->half[h].last - v.window || tok0 + 127 < v.sinks);
+                if (!all_seen) {
+                    // columns [0, up) are not after the row; of them [0, front) are sinks and [low, up) in the window
+                    const int up = pos - tok0 + 1, low = v.window > 0 ? pos - v.window + 1 - tok0 : 0, front = v.sinks - tok0;
+#pragma unroll
+                    for (int g = 0; g < 4; g++) {
+                        uint32_t seen = bits_below(up - 32 * g) & (~bits_below(low - 32 * g) | bits_below(front - 32 * g));
+                        if ((bad >> (2 * g)) & 1u) seen &= 0xffff0000u;
+                        if ((bad >> (2 * g + 1)) & 1u) seen &= 0x0000ffffu;
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            if (!((seen >> c) & 1u)) s[g][c] = 0xff800000u;
+                    }
+                }
+                float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 128; c++) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c >> 5][c & 31]));
+                const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
+                if (t == t0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, top > m + 8.0f)) {
+                    // the product of the tile before is complete (this S came after it)
+                    const float nm = fmaxf(m, top), fac = nm == -INFINITY ? 1.0f : ex2(m - nm);
+                    m = nm;
+                    l *= fac;
+#pragma unroll 1
+                    for (int c = 0; c < DP / 16; c++) {
+                        uint32_t o[16];
+                        tmem_ld_x16(o_addr + 16 * c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
+                        tmem_st_x16(o_addr + 16 * c, o);
+                    }
+                }
+                const float u = m == -INFINITY ? 0.0f : m;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int hf = 0; hf < 4; hf++) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int c = 0; c < 16; c++) {
+                        const float a = ex2(__fmaf_rn(__uint_as_float(s[hf][2 * c]), p.scale_log2, -u));
+                        const float b = ex2(__fmaf_rn(__uint_as_float(s[hf][2 * c + 1]), p.scale_log2, -u));
+                        sum[(2 * c) & 3] += a;
+                        sum[(2 * c + 1) & 3] += b;
+                        w[c] = pack2<F16>(a, b);
+                    }
+                    tmem_st_x16(s_addr + 16 * hf, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_ready[h]);
+            }
+            if (!ok) break;
+            // ---- epilogue ----
+            if (has) {
+                ok = chunk_wait(&bars->o_full[h], n_o & 1, bars, p);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                n_o++;
+                tc_fence_after();
+            }
+            const bool whole = it->whole;
+            const int slot = 2 * (int)cta + (items == 0 ? 0 : 1), pr = h * 128 + row;
+            float *part = p.part + (int64_t)slot * C::kSlotFloats;
+            const int64_t orow = valid ? tensor_row(it, pr) : 0;
+            const float inv = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+#pragma unroll 1
+            for (int c = 0; c < DP / 32; c++) {
+                uint32_t o[32];
+                if (has) {
+                    tmem_ld_32x32b_x32(o_addr + 32 * c, o);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i++) o[i] = 0u;
+                }
+                if (!valid) continue;
+                if (whole) {
+                    const int64_t at = orow * v.head_dim + 32 * c;
+                    uint16_t *dst = static_cast<uint16_t *>(p.out) + at;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        if (32 * c + 8 * i >= v.head_dim ||
+                            !QLORA_IN(at + 8 * i + 7, (int64_t)v.tokens * v.heads * v.head_dim))
+                            break;
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            w[j] = pack2<F16>(__uint_as_float(o[8 * i + 2 * j]) * inv, __uint_as_float(o[8 * i + 2 * j + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(dst + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        *reinterpret_cast<uint4 *>(part + pr * DP + 32 * c + 4 * i) =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+            if (valid && whole && p.lse) p.lse[orow] = l > 0.0f ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
+            if (valid && !whole) {
+                part[C::kRows * DP + pr] = m;
+                part[C::kRows * DP + C::kRows + pr] = l;
+            }
+            if (it->begins && threadIdx.x == 0) p.desc[cta] = Desc{it->b, it->h, it->rt, slot, (int)cta, it->parts};
+            tc_fence_before();   // these reads of O come before the next item's first product, behind p_ready
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->item_empty[items & 3]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace attn
+}  // namespace qlora

@@ -184,6 +184,92 @@ def test_most_requests(q):
     Case(q, lens, [1] * 4096, 1, 1, 16, 16, seed=7).run().check()
 
 
+@pytest.mark.parametrize("D", [16, 64, 80, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_chunk_types_and_dims(q, D, dtype):
+    Case(q, [300, 17, 0, 129], [60, 17, 2, 1], 4, 2, D, 16, dtype, seed=30).run().check()
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (3, 3), (8, 1), (14, 2), (12, 4)])
+@pytest.mark.parametrize("page,order", [(16, "heads first"), (32, "tokens first"), (128, "heads first"), (256, "tokens first")])
+def test_chunk_heads_pages_and_orders(q, heads, kv_heads, page, order):
+    Case(q, [400, 5, 130, 700], [150, 5, 128, 33], heads, kv_heads, 128, page, order=order, seed=31).run().check()
+
+
+@pytest.mark.parametrize("n", [17, 31, 127, 128, 129, 255, 256, 257, 300])
+def test_chunk_rows(q, n):
+    Case(q, [n + 77, n], [n, n], 1, 1, 64, 16, seed=32).run().check()
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (16, 1), (100, 4), (130, 200), (256, 128), (5000, 4)])
+def test_chunk_window(q, window, sinks):
+    Case(q, [900, 300, 40], [200, 300, 1], 4, 2, 64, 32, seed=33).run(window, sinks).check(window, sinks)
+
+
+def test_chunk_rows_without_a_key(q):
+    """Rows before position 0, requests without any position, and many of them in a row."""
+    Case(q, [3, 0, 0, 0, 0, 0, 0, 40, 0], [60, 20, 1, 300, 2, 2, 5, 20, 9], 4, 4, 64, 16, seed=34).run().check()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_chunk_whole_prompt(q, dtype):
+    c = Case(q, [2048], [2048], 4, 4, 128, 16, dtype, seed=35).run()
+    c.check(rows=[0, 1, 2, 127, 128, 129, 255, 256, 1000, 1023, 1024, 2047])
+    first = c.out.clone()
+    assert torch.equal(c.run().out, first)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (3000, 20)])
+def test_chunk_over_a_long_context_is_split(q, window, sinks):
+    c = Case(q, [20011, 64], [40, 64], 4, 2, 128, 64, seed=36).run(window, sinks)
+    c.check(window, sinks, rows=[0, 1, 20, 39, 40, 63])
+
+
+def test_chunk_many_requests(q):
+    rng = np.random.default_rng(37)
+    lens = rng.integers(0, 150, 700).tolist()
+    Case(q, lens, [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 30, 700))], 2, 1, 64, 16, seed=37).run().check(
+        rows=[0, 7, 15, 29])
+
+
+def test_chunk_growing_scores(q):
+    """Keys that grow along the context: the running maximum is passed again and again."""
+    c = Case(q, [700], [64], 2, 1, 64, 16, torch.float16, seed=38)
+    ramp = torch.linspace(0.05, 6.0, 700, device="cuda")[:, None, None]
+    c.kd[0] = (c.kd[0].abs() * ramp).to(torch.float16)
+    c.qt = c.qt.abs()
+    for i in range(44):
+        n = min(16, 700 - 16 * i)
+        c.cache.k[int(c.table[0, i]), :, :n] = c.kd[0][16 * i:16 * i + n].transpose(0, 1)
+    c.run().check()
+
+
+def test_kernels_agree(q):
+    """The bound on q_len chooses the kernel, not the result: both stay within
+    their bounds of the oracle, so within the sum of them of each other."""
+    a = Case(q, [300, 40, 1000], [2, 1, 3], 8, 4, 128, 16, seed=39).run()
+    b = Case(q, [300, 40, 1000], [2, 1, 3], 8, 4, 128, 16, seed=39, max_q_len=0).run()
+    assert not torch.equal(a.out, b.out)
+    diff, size = (a.out.float() - b.out.float()).abs()[:6], a.out.float().abs()[:6]
+    # half a step each, and half a step of a weight on values of at most 4 deviations
+    assert (diff <= 2.0 ** -7 * size + 2.0 ** -8 * 4).all()
+
+
+def test_chunk_bad_pages_are_left_out(q):
+    c = Case(q, [200, 90, 64], [100, 2, 30], 4, 2, 64, 16, seed=40)
+    present = [np.ones(200, bool), np.ones(90, bool), np.zeros(64, bool)]
+    for b, i, v in [(0, 0, -1), (0, 3, c.cache.num_pages), (0, 12, 2 ** 31 - 1), (1, 5, -2 ** 31), (1, 0, -7)]:
+        c.table[b, i] = v
+        present[b][16 * i:16 * i + 16] = False
+    c.table[2] = c.cache.num_pages
+    c.run().check(present=present)
+
+
+def test_chunk_positions_beyond_the_table_are_left_out(q):
+    c = Case(q, [200, 90], [70, 20], 4, 2, 64, 16, seed=41, width=6)
+    c.run().check(present=[np.arange(200) < 96, np.arange(90) < 96])
+
+
 def test_bad_pages_are_left_out(q):
     c = Case(q, [200, 90, 64], [1, 2, 1], 4, 2, 64, 16, seed=8)
     present = [np.ones(200, bool), np.ones(90, bool), np.zeros(64, bool)]
