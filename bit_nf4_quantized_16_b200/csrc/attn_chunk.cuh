@@ -4,14 +4,14 @@
 // One CTA per SM, persistent over its items of 256 rows x tiles of 128
 // positions.  The rows form two halves of 128, A and B, whose softmax alternates
 // with the other half's products:
-//   warps 0-3, 4-7  softmax of half A, B: one thread per row
-//   warp 8          the schedule (it hands the items to the other warps through
+//   warps 0-7, 8-15 softmax of half A, B: two threads per row, 64 positions each
+//   warp 16         the schedule (it hands the items to the other warps through
 //                   a ring in shared memory), and keys and values: a ring of
 //                   tiles filled by TMA page by page
-//   warp 9          issues the products
-//   warps 10, 11    query rows of half A, B
+//   warp 17         issues the products
+//   warps 18, 19    query rows of half A, B
 // Scores S = Q K^T (tcgen05, both operands in shared memory) land in tensor
-// memory; a softmax thread reads its row, and writes the weights as 16-bit
+// memory; the softmax threads read their row, and write the weights as 16-bit
 // values over the scores, where the second product O += P V takes them as its
 // left operand: they never pass through shared memory.  512 columns of
 // tensor memory hold S/P and O of both halves.  The order of issue is
@@ -34,16 +34,17 @@ namespace attn {
 
 template <int DP>
 struct ChunkCfg {
-    static constexpr int kThreads = 384, kRows = 256, kTile = 128, kOv = 1;
+    static constexpr int kThreads = 640, kRows = 256, kTile = 128, kOv = 1;
     static constexpr uint32_t kQBytes = 128 * DP * 2;      // one half
     static constexpr uint32_t kTileBytes = 128 * DP * 2;   // keys or values of one tile
     static constexpr int kStages = DP == 128 ? 5 : 8;
     static constexpr uint32_t kRingOff = 2 * kQBytes;
     static constexpr uint32_t kBarOff = kRingOff + kStages * kTileBytes;
-    static constexpr uint32_t kBytes = kBarOff + 1024 + 1024;   // + alignment slack
+    static constexpr uint32_t kMaxOff = kBarOff + 1024;    // [half][64-position part][row]: maxima, then sums
+    static constexpr uint32_t kBytes = kMaxOff + 2048;
     static constexpr int kSlotFloats = kRows * DP + 2 * kRows;
     static constexpr uint32_t kOCol = 256;                 // O_A, O_B at 256 + DP * half; S at 128 * half
-    static constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 2 * 208 + 88 = 3 * 168, the launch's share
+    static constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;   // 4 * 104 + 64 = 5 * 96, the launch's share
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -53,14 +54,36 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// D[tmem] (+)= A[tmem, K-major 16-bit] * B[smem desc]
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// The products of this kernel.  Descriptors of one operand differ in the low
+// word only (the start address), so a step costs one addition: the issuing
+// thread has no time for more (64 cycles per product).
+template <bool kAccumulate>
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem, K-major 16-bit] * B[smem desc]
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                          uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -86,17 +109,14 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// One half of an item: its rows' positions, and which of the CTA's tiles it needs.
+// One half of an item: its rows' positions, and the CTA's tiles that it takes:
+// from the first to the last that any of its rows sees.
 struct Half {
     int rows, first, last;   // valid rows (0: none), position of the first and the last
-    int t_first, t_last;     // first and last tile needed of [t0, t1); t_last < t_first: none
+    int t_first, t_last;     // tiles; t_last < t_first: none
 
-    __device__ __forceinline__ bool needs(const BatchView &v, int tile) const
-    {
-        const int a = tile * 128;
-        return a <= last && (v.window <= 0 || a + 127 > first - v.window || a < v.sinks);
-    }
     __device__ __forceinline__ bool has() const { return t_last >= t_first; }
+    __device__ __forceinline__ bool takes(int t) const { return t >= t_first && t <= t_last; }
 };
 
 __device__ __forceinline__ Half half_of(const BatchView &v, const Item &it, int half)
@@ -109,8 +129,12 @@ __device__ __forceinline__ Half half_of(const BatchView &v, const Item &it, int 
     if (f.rows == 0) return f;
     item_positions<128>(v, it.r, it.rt * 2 + half, f.first, f.last);
     f.t_last = it.t1 - 1;
-    while (f.t_last >= f.t_first && !f.needs(v, it.tiles.at(f.t_last))) f.t_last--;
-    while (f.t_last >= f.t_first && !f.needs(v, it.tiles.at(f.t_first))) f.t_first++;
+    auto sees = [&](int t) {
+        const int a = it.tiles.at(t) * 128;
+        return a <= f.last && (v.window <= 0 || a + 127 > f.first - v.window || a < v.sinks);
+    };
+    while (f.t_last >= f.t_first && !sees(f.t_last)) f.t_last--;
+    while (f.t_last >= f.t_first && !sees(f.t_first)) f.t_first++;
     return f;
 }
 
@@ -160,20 +184,23 @@ __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, Chunk
 }
 
 template <int DP, bool F16>
-__global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ AttnParams p)
 {
     using C = ChunkCfg<DP>;
     using W = Walker<C::kThreads, C::kRows, C::kTile, C::kOv>;
     using namespace sm100;
     constexpr int ST = C::kStages;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     ChunkBars *bars = reinterpret_cast<ChunkBars *>(smem + C::kBarOff);
     static_assert(sizeof(ChunkBars) <= 1024, "barriers and items fit their place");
     int64_t *pre = reinterpret_cast<int64_t *>(smem + C::kRingOff);   // before the ring is used
     const BatchView &v = p.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    if (smem_u32(smem) & 1023u) {   // the swizzled tiles need this; all of the memory is used, so none is left to align with
+        if (threadIdx.x == 0) atomicExch(p.err, 1);
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; s++) {
             mbar_init(&bars->kv_full[s], 1);
@@ -181,14 +208,14 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
         }
         for (int h = 0; h < 2; h++) {
             mbar_init(&bars->s_full[h], 1);
-            mbar_init(&bars->p_ready[h], 4);
+            mbar_init(&bars->p_ready[h], 8);
             mbar_init(&bars->o_full[h], 1);
             mbar_init(&bars->q_full[h], 1);
             mbar_init(&bars->q_free[h], 1);
         }
         for (int i = 0; i < 4; i++) {
             mbar_init(&bars->item_full[i], 1);
-            mbar_init(&bars->item_empty[i], 11);   // 8 softmax warps, the products, 2 warps of query rows
+            mbar_init(&bars->item_empty[i], 19);   // 16 softmax warps, the products, 2 warps of query rows
         }
         mbar_init(&bars->tail, 1);
         mbar_init(&bars->drain, 1);
@@ -197,7 +224,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
         tma_prefetch_desc(&p.tk);
         tma_prefetch_desc(&p.tv);
     }
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_alloc(&bars->tmem, 512);
         tmem_relinquish();
     }
@@ -211,7 +238,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
     if (threadIdx.x == 0) p.desc[cta].parts = 0;
     const uint32_t tmem = bars->tmem;
     W walk;
-    if (warp == 8) {
+    if (warp == 16) {
         walk.init(v, pre, cta < G ? cta * total / G : 0, cta < G ? (cta + 1) * total / G : 0, p.whole_items);
         fence_proxy_async_smem();
     }
@@ -220,7 +247,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
     // The n-th item of this CTA, or null at the end or after a failure.
     auto item_at = [&](uint32_t n) -> const ChunkItem * {
         bool ok = chunk_wait(&bars->item_full[n & 3], (n >> 2) & 1, bars, p);
-        if (warp != 9) ok = __all_sync(0xffffffffu, ok);   // the products' warp runs one thread
+        if (warp != 17) ok = __all_sync(0xffffffffu, ok);   // the products' warp runs one thread
         if (!ok) return nullptr;
         const ChunkItem *it = &bars->item[n & 3];
         return it->h < 0 ? nullptr : it;
@@ -231,9 +258,9 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
         return (int64_t)(it->q0 + g / v.group) * v.heads + it->h * v.group + g % v.group;
     };
 
-    if (warp >= 8) {
+    if (warp >= 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-        if (warp == 8) {
+        if (warp == 16) {
             // ---- schedule; keys and values, in the order K(0) V(0) K(1) V(1) ... ----
             const int box = min(1 << v.page_shift, 128), pieces = 128 / box;
             uint32_t n = 0, tiles = 0, tails = 0, items = 0;   // ring entries, tiles, tail waits, items so far
@@ -324,86 +351,119 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                     mbar_wait_bounded(&bars->kv_full[j % ST], (j / ST) & 1, p.timeout_ns / 8);
                 mbar_wait_bounded(&bars->tail, tails & 1, p.timeout_ns / 8);
             }
-        } else if (warp == 9) {
+        } else if (warp == 17) {
             // ---- products ----
             if (lane == 0) {
                 const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0, F16), idesc_o = idesc_bf16_f32(128, DP, 0, 1, F16);
-                const uint32_t ring = smem_u32(smem + C::kRingOff), qbase = smem_u32(smem);
-                const int k_steps = v.head_dim / 16;
-                uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // weights and query tiles taken
+                const uint64_t qd = smem_desc_sw128(smem_u32(smem), 16, 1024),
+                               kd = smem_desc_sw128(smem_u32(smem + C::kRingOff), 16, 1024),
+                               vd = smem_desc_sw128(smem_u32(smem + C::kRingOff), 16384, 1024);
+                const uint32_t q_desc = (uint32_t)qd, k_desc = (uint32_t)kd, v_desc = (uint32_t)vd, hi = (uint32_t)(qd >> 32);
+                uint32_t n_p = 0, n_q = 0;   // bit h: parity of the next weights, query rows of half h
                 bool ok = true;
                 auto wait = [&](uint64_t *bar, uint32_t parity) {
                     if (ok) ok = chunk_wait(bar, parity, bars, p);
                     if (ok) tc_fence_after();
                 };
-                // S runs one tile ahead of PV, across items.  An item is given back before the
-                // next one is waited for: PV keeps a copy of what it needs.
-                const ChunkItem *si = nullptr;   // the item of the next tile of S
-                uint32_t items = 0;              // items begun
-                int st = 0;
+                // S runs one tile ahead of PV, across items.  The thread keeps what it needs of
+                // both tiles' items in registers: what it does between two products is
+                // latency that nothing hides.
+                struct Range {
+                    int first, last;
+                };
+                Range sr[2] = {}, pr[2] = {};
+                bool more = true, crossed = false;   // is there a tile for S; is it of another item than PV's
+                uint32_t items = 0;                  // items begun
+                int st = -1, s_end = 0;
                 auto next_tile = [&]() {
+                    crossed = false;
                     st++;
-                    while (!si || st >= si->t1) {
-                        if (si) mbar_arrive(&bars->item_empty[(items - 1) & 3]);
-                        si = item_at(items++);
-                        if (!si) return;
-                        st = si->t0;
+                    while (st >= s_end) {
+                        if (items) mbar_arrive(&bars->item_empty[(items - 1) & 3]);
+                        const ChunkItem *it = item_at(items++);
+                        crossed = true;
+                        more = it != nullptr;
+                        if (!more) return;
+                        st = it->t0;
+                        s_end = it->t1;
+#pragma unroll
+                        for (int h = 0; h < 2; h++) sr[h] = Range{it->half[h].t_first, it->half[h].t_last};
                     }
                 };
-                auto issue_scores = [&](int h, uint32_t slot) {
-                    const Half &f = si->half[h];
-                    if (!f.has() || !f.needs(v, si->tiles.at(st))) return;
-                    if (st == f.t_first) {
-                        wait(&bars->q_full[h], nq[h] & 1);
-                        nq[h]++;
+                auto scores = [&](int h, uint32_t slot) {
+                    if (st < sr[h].first || st > sr[h].last) return;
+                    if (st == sr[h].first) {
+                        wait(&bars->q_full[h], (n_q >> h) & 1);
+                        n_q ^= 1u << h;
                     }
                     if (!ok) return;
-                    for (int kk = 0; kk < k_steps; kk++) {
-                        const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
-                        tc_mma_bf16(tmem + 128 * h, smem_desc_sw128(qbase + h * C::kQBytes + o, 16, 1024),
-                                    smem_desc_sw128(ring + slot * C::kTileBytes + o, 16, 1024), idesc_s, kk > 0);
+                    const uint32_t d = tmem + 128 * h, q_lo = q_desc + h * (C::kQBytes >> 4),
+                                   k_lo = k_desc + slot * (C::kTileBytes >> 4);
+                    tc_mma_ss<false>(d, q_lo, k_lo, hi, idesc_s);
+#pragma unroll
+                    for (int kk = 1; kk < DP / 16; kk++) {
+                        const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                        tc_mma_ss<true>(d, q_lo + o, k_lo + o, hi, idesc_s);
                     }
                     tc_commit(&bars->s_full[h]);
-                    if (st == f.t_last) tc_commit(&bars->q_free[h]);
+                    if (st == sr[h].last) tc_commit(&bars->q_free[h]);
                 };
-                uint32_t e = 0;   // ring entry of K of the tile of S
-                next_tile();
-                if (si) {
-                    wait(&bars->kv_full[0], 0);
-                    issue_scores(0, 0);
-                    issue_scores(1, 0);
-                    if (ok) tc_commit(&bars->kv_empty[0]);
-                }
-                while (si && ok) {
-                    // PV of this tile, S of the next
-                    const Half pf[2] = {si->half[0], si->half[1]};
-                    const int pt = st, tile = si->tiles.at(st);
-                    const uint32_t ve = (e + 1) % ST, ke = (e + 2) % ST;
-                    next_tile();
-                    bool k_here = false;
-                    wait(&bars->kv_full[ve], ((e + 1) / ST) & 1);
-                    for (int h = 0; h < 2 && ok; h++) {
-                        const Half &f = pf[h];
-                        if (f.has() && f.needs(v, tile)) {
-                            wait(&bars->p_ready[h], np[h] & 1);
-                            np[h]++;
-                            if (!ok) break;
+                auto values = [&](int h, int t, uint32_t slot) {
+                    if (t < pr[h].first || t > pr[h].last) return;
+                    wait(&bars->p_ready[h], (n_p >> h) & 1);
+                    n_p ^= 1u << h;
+                    if (!ok) return;
+                    const uint32_t d = tmem + C::kOCol + DP * h, a = tmem + 128 * h,
+                                   v_lo = v_desc + slot * (C::kTileBytes >> 4);
+                    tc_mma_ts(d, a, v_lo, hi, idesc_o, t > pr[h].first);
 #pragma unroll
-                            for (int kk = 0; kk < 8; kk++)
-                                tc_mma_ts(tmem + C::kOCol + DP * h, tmem + 128 * h + 8 * kk,
-                                          smem_desc_sw128(ring + ve * C::kTileBytes + 2048 * kk, 16384, 1024), idesc_o,
-                                          pt > f.t_first || kk > 0);
-                            if (pt == f.t_last) tc_commit(&bars->o_full[h]);
-                        }
-                        if (h == 1) tc_commit(&bars->kv_empty[ve]);
-                        if (si) {
-                            if (!k_here) wait(&bars->kv_full[ke], ((e + 2) / ST) & 1);
-                            k_here = true;
-                            if (ok) issue_scores(h, ke);
-                            if (h == 1 && ok) tc_commit(&bars->kv_empty[ke]);
-                        }
+                    for (int kk = 1; kk < 8; kk++) tc_mma_ts(d, a + 8 * kk, v_lo + (2048 >> 4) * kk, hi, idesc_o, 1);
+                    if (t == pr[h].last) tc_commit(&bars->o_full[h]);
+                };
+                uint32_t slot = 0, phase = 0;   // of the next ring entry
+                auto advance = [&]() {
+                    const uint32_t s = slot;
+                    wait(&bars->kv_full[s], phase);
+                    if (++slot == ST) {
+                        slot = 0;
+                        phase ^= 1;
                     }
-                    e += 2;
+                    return s;
+                };
+                next_tile();
+                if (more) {
+                    const uint32_t ks = advance();
+                    scores(0, ks);
+                    scores(1, ks);
+                    if (ok) tc_commit(&bars->kv_empty[ks]);
+                }
+                while (more && ok) {
+                    // PV of this tile, S of the next
+                    const int t = st;
+                    pr[0] = sr[0];
+                    pr[1] = sr[1];
+                    next_tile();
+                    const uint32_t vs = advance();
+                    if (!crossed) {
+                        const uint32_t ks = advance();
+                        values(0, t, vs);
+                        if (ok) scores(0, ks);
+                        if (ok) values(1, t, vs);
+                        if (!ok) break;
+                        tc_commit(&bars->kv_empty[vs]);
+                        scores(1, ks);
+                        if (ok) tc_commit(&bars->kv_empty[ks]);
+                    } else {   // the next item's query rows may still be on their way
+                        if (ok) values(0, t, vs);
+                        if (ok) values(1, t, vs);
+                        if (!ok) break;
+                        tc_commit(&bars->kv_empty[vs]);
+                        if (!more) break;
+                        const uint32_t ks = advance();
+                        if (ok) scores(0, ks);
+                        if (ok) scores(1, ks);
+                        if (ok) tc_commit(&bars->kv_empty[ks]);
+                    }
                 }
                 if (!ok) {
                     // wait (bounded) until the products already issued finish
@@ -413,7 +473,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
             }
         } else {
             // ---- query rows of one half ----
-            const int h = warp - 10;
+            const int h = warp - 18;
             uint8_t *dst = smem + h * C::kQBytes;
             uint32_t n = 0, items = 0;
             bool ok = true;
@@ -423,17 +483,28 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                     if (n > 0) ok = chunk_wait(&bars->q_free[h], (n - 1) & 1, bars, p);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-#pragma unroll 4
-                    for (int i = lane; i < 128 * (DP / 8); i += 32) {
-                        const int r = i / (DP / 8), ch = i % (DP / 8);
-                        const bool in = r < f.rows && ch * 8 < v.head_dim;
-                        const int64_t o = in ? tensor_row(it, h * 128 + r) * v.head_dim + ch * 8 : 0;
-                        const bool there = in && QLORA_IN(o + 7, (int64_t)v.tokens * v.heads * v.head_dim);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                         smem_u32(dst + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4))),
-                                     "l"(static_cast<const uint16_t *>(p.q) + o), "r"(there ? 16 : 0)
-                                     : "memory");
+                    // this lane's part of the rows 32 i + lane: where they begin, or -1
+                    int64_t begin[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int r = 32 * i + lane;
+                        begin[i] = r < f.rows ? tensor_row(it, h * 128 + r) * v.head_dim : -1;
                     }
+                    constexpr int kPerRow = DP / 8, kRowsAtOnce = 32 / kPerRow;   // 16-byte pieces
+                    const int ch = lane % kPerRow;
+                    const bool in = ch * 8 < v.head_dim;
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+#pragma unroll 8
+                        for (int j = 0; j < 32; j += kRowsAtOnce) {
+                            const int rr = j + lane / kPerRow, r = 32 * i + rr;
+                            const int64_t o = __shfl_sync(0xffffffffu, begin[i], rr) + ch * 8;
+                            const bool there = in && o >= ch * 8 && QLORA_IN(o + 7, (int64_t)v.tokens * v.heads * v.head_dim);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                             smem_u32(dst + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4))),
+                                         "l"(static_cast<const uint16_t *>(p.q) + (there ? o : 0)), "r"(there ? 16 : 0)
+                                         : "memory");
+                        }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     fence_proxy_async_smem();
                     n++;
@@ -448,38 +519,48 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         // ---- softmax and epilogue of one half ----
-        const int h = warp >> 2, row = threadIdx.x & 127;
+        // Warps w and w + 4 of a half share rows: w takes positions 0-63 of a tile, w + 4 the rest.
+        const int h = warp >> 3, part = (warp >> 2) & 1, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t s_addr = tmem + lanes + 128 * h, o_addr = tmem + lanes + C::kOCol + DP * h;
+        const uint32_t s_addr = tmem + lanes + 128 * h, o_addr = tmem + lanes + C::kOCol + DP * h + (DP / 2) * part;
+        float *mine = reinterpret_cast<float *>(smem + C::kMaxOff) + (h * 2 + part) * 128 + row;
+        const float *other = reinterpret_cast<const float *>(smem + C::kMaxOff) + (h * 2 + (part ^ 1)) * 128 + row;
+        const int pair_bar = 1 + h * 4 + (warp & 3);
+        // The two warps meet at a barrier without a time limit, so neither may leave the other
+        // there: a warp that gives up arrives once more, and each looks for a failure before
+        // every meeting.  The arrival comes after the failure is marked, so a warp that met
+        // it sees the mark before the next meeting.
+        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
+        auto failed = [&]() { return __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&bars->abort)) != 0; };
         uint32_t n_s = 0, n_o = 0, tiles = 0;
         bool ok = true;
         const ChunkItem *it;
         for (uint32_t items = 0; ok && (it = item_at(items)); items++) {
-            const bool valid = row < it->half[h].rows;
-            const int t0 = it->half[h].t_first, t1 = it->half[h].t_last;
-            const bool has = t1 >= t0;
+            const Half f = it->half[h];
+            const bool valid = row < f.rows, has = f.has();
             const int pos = valid ? it->pos0 + (it->row0 + h * 128 + row) / v.group : -1;
+            const int t_end = it->t1, t_begin = it->t0;
             float m = -INFINITY, l = 0.0f;   // m: the maximum that the weights are taken against
-            for (int t = it->t0; t < it->t1; t++, tiles++) {
-                const int tile = it->tiles.at(t), tok0 = tile * 128;
-                if (!has || !it->half[h].needs(v, tile)) continue;
+            for (int t = t_begin; t < t_end; t++, tiles++) {
+                if (!f.takes(t)) continue;
+                const int tok0 = it->tiles.at(t) * 128 + 64 * part;
                 ok = chunk_wait(&bars->s_full[h], n_s & 1, bars, p);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, ok && !*reinterpret_cast<volatile int *>(&bars->abort));
                 if (!ok) break;
                 n_s++;
                 tc_fence_after();
-                uint32_t s[4][32];
+                const uint32_t bad = (bars->bad[tiles & 7] >> (4 * part)) & 15u;
+                uint32_t s[2][32];
 #pragma unroll
-                for (int c = 0; c < 4; c++) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);
+                for (int c = 0; c < 2; c++) tmem_ld_32x32b_x32(s_addr + 64 * part + 32 * c, s[c]);
                 tmem_ld_wait();
-                const uint32_t bad = bars->bad[tiles & 7];
-                const bool all_seen = tok0 + 127 <= it->half[h].first && bad == 0 &&
-                                      (v.window <= 0 || tok0 > it->half[h].last - v.window || tok0 + 127 < v.sinks);
+                const bool all_seen = tok0 + 63 <= f.first && bad == 0 &&
+                                      (v.window <= 0 || tok0 > f.last - v.window || tok0 + 63 < v.sinks);
                 if (!all_seen) {
                     // columns [0, up) are not after the row; of them [0, front) are sinks and [low, up) in the window
                     const int up = pos - tok0 + 1, low = v.window > 0 ? pos - v.window + 1 - tok0 : 0, front = v.sinks - tok0;
 #pragma unroll
-                    for (int g = 0; g < 4; g++) {
+                    for (int g = 0; g < 2; g++) {
                         uint32_t seen = bits_below(up - 32 * g) & (~bits_below(low - 32 * g) | bits_below(front - 32 * g));
                         if ((bad >> (2 * g)) & 1u) seen &= 0xffff0000u;
                         if ((bad >> (2 * g + 1)) & 1u) seen &= 0x0000ffffu;
@@ -490,9 +571,15 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 }
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 128; c++) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c >> 5][c & 31]));
-                const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
-                if (t == t0) {
+                for (int c = 0; c < 32; c++) x[c & 3] = max3(x[c & 3], __uint_as_float(s[0][c]), __uint_as_float(s[1][c]));
+                float top = fmaxf(max3(x[0], x[1], x[2]), x[3]);
+                // the other thread's maximum of the row.  (Its next write waits for S of the next
+                // tile, so for the weights of this one, so for this read.)  The barrier also says
+                // that both have their scores in registers: the weights overwrite them.
+                *mine = top;
+                pair_sync();
+                top = fmaxf(top, *other) * p.scale_log2;
+                if (t == f.t_first) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, top > m + 8.0f)) {
                     // the product of the tile before is complete (this S came after it)
@@ -500,7 +587,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                     m = nm;
                     l *= fac;
 #pragma unroll 1
-                    for (int c = 0; c < DP / 16; c++) {
+                    for (int c = 0; c < DP / 32; c++) {
                         uint32_t o[16];
                         tmem_ld_x16(o_addr + 16 * c, o);
                         tmem_ld_wait();
@@ -512,40 +599,43 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 const float u = m == -INFINITY ? 0.0f : m;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int hf = 0; hf < 4; hf++) {
+                for (int g = 0; g < 2; g++) {
                     uint32_t w[16];
 #pragma unroll
                     for (int c = 0; c < 16; c++) {
-                        const float a = ex2(__fmaf_rn(__uint_as_float(s[hf][2 * c]), p.scale_log2, -u));
-                        const float b = ex2(__fmaf_rn(__uint_as_float(s[hf][2 * c + 1]), p.scale_log2, -u));
+                        const float a = ex2(__fmaf_rn(__uint_as_float(s[g][2 * c]), p.scale_log2, -u));
+                        const float b = ex2(__fmaf_rn(__uint_as_float(s[g][2 * c + 1]), p.scale_log2, -u));
                         sum[(2 * c) & 3] += a;
                         sum[(2 * c + 1) & 3] += b;
                         w[c] = pack2<F16>(a, b);
                     }
-                    tmem_st_x16(s_addr + 16 * hf, w);
+                    tmem_st_x16(s_addr + 32 * part + 16 * g, w);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->p_ready[h]);
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
             if (!ok) break;
-            // ---- epilogue ----
-            if (has) {
+            // ---- epilogue: this thread's half of the row's columns ----
+            const bool whole = it->whole;
+            const int slot = 2 * (int)cta + (items == 0 ? 0 : 1), pr = h * 128 + row;
+            float *out_part = p.part + (int64_t)slot * C::kSlotFloats;
+            const int64_t orow = valid ? tensor_row(it, pr) : 0;
+            if (has) {   // complete: so the other thread is done with the last tile's maximum
                 ok = chunk_wait(&bars->o_full[h], n_o & 1, bars, p);
                 ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
                 n_o++;
                 tc_fence_after();
             }
-            const bool whole = it->whole;
-            const int slot = 2 * (int)cta + (items == 0 ? 0 : 1), pr = h * 128 + row;
-            float *part = p.part + (int64_t)slot * C::kSlotFloats;
-            const int64_t orow = valid ? tensor_row(it, pr) : 0;
+            if (!ok || !(ok = !failed())) break;
+            *mine = l;
+            pair_sync();
+            l += *other;
             const float inv = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
 #pragma unroll 1
-            for (int c = 0; c < DP / 32; c++) {
+            for (int c = 0; c < DP / 64; c++) {
                 uint32_t o[32];
                 if (has) {
                     tmem_ld_32x32b_x32(o_addr + 32 * c, o);
@@ -555,13 +645,13 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                     for (int i = 0; i < 32; i++) o[i] = 0u;
                 }
                 if (!valid) continue;
+                const int col = (DP / 2) * part + 32 * c;
                 if (whole) {
-                    const int64_t at = orow * v.head_dim + 32 * c;
+                    const int64_t at = orow * v.head_dim + col;
                     uint16_t *dst = static_cast<uint16_t *>(p.out) + at;
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        if (32 * c + 8 * i >= v.head_dim ||
-                            !QLORA_IN(at + 8 * i + 7, (int64_t)v.tokens * v.heads * v.head_dim))
+                        if (col + 8 * i >= v.head_dim || !QLORA_IN(at + 8 * i + 7, (int64_t)v.tokens * v.heads * v.head_dim))
                             break;
                         uint32_t w[4];
 #pragma unroll
@@ -572,24 +662,29 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; i++)
-                        *reinterpret_cast<uint4 *>(part + pr * DP + 32 * c + 4 * i) =
+                        *reinterpret_cast<uint4 *>(out_part + pr * DP + col + 4 * i) =
                             make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
             }
-            if (valid && whole && p.lse) p.lse[orow] = l > 0.0f ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
-            if (valid && !whole) {
-                part[C::kRows * DP + pr] = m;
-                part[C::kRows * DP + C::kRows + pr] = l;
+            if (valid && part == 0) {
+                if (!whole) {
+                    out_part[C::kRows * DP + pr] = m;
+                    out_part[C::kRows * DP + C::kRows + pr] = l;
+                } else if (p.lse) {
+                    p.lse[orow] = l > 0.0f ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
+                }
             }
             if (it->begins && threadIdx.x == 0) p.desc[cta] = Desc{it->b, it->h, it->rt, slot, (int)cta, it->parts};
             tc_fence_before();   // these reads of O come before the next item's first product, behind p_ready
-            __syncwarp();
+            if (!(ok = !failed())) break;
+            pair_sync();         // the sums have been read: the next maxima may take their place
             if (lane == 0) mbar_arrive(&bars->item_empty[items & 3]);
         }
+        if (failed()) asm volatile("bar.arrive %0, 64;" ::"r"(pair_bar) : "memory");
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

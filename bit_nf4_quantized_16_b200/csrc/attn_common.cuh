@@ -136,11 +136,11 @@ struct Item {
 };
 
 // Exclusive prefix of the units of NT runs of consecutive requests, in shared
-// memory (pre[NT] = total).  Called by all NT threads.
+// memory (pre[NT] = total; NT / 32 values more are scratch).  Called by all NT threads.
 template <int NT, int ROWS, int TILE, int OV>
 __device__ __forceinline__ void schedule_scan(const BatchView &v, int64_t *pre)
 {
-    __shared__ int64_t warp_sum[NT / 32];
+    int64_t *warp_sum = pre + NT + 1;
     const int tid = threadIdx.x, lane = tid & 31, run = (v.batch + NT - 1) / NT;
     int64_t mine = 0;
     for (int b = tid * run; b < min((tid + 1) * run, v.batch); b++)

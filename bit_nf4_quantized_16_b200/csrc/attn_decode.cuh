@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
     using namespace sm100;
     constexpr int ST = C::kStages;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t pre[C::kThreads + 1];
+    __shared__ int64_t pre[C::kThreads + 1 + C::kWarps];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const BatchView &v = p.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
