@@ -4,14 +4,14 @@
 // One CTA per SM, persistent over its items of 256 rows x tiles of 128
 // positions.  The rows form two halves of 128, A and B, whose softmax alternates
 // with the other half's products:
-//   warps 0-7, 8-15 softmax of half A, B: two threads per row, 64 positions each
-//   warp 16         the schedule (it hands the items to the other warps through
+//   warps 0-3, 4-7  softmax of half A, B: one thread per row
+//   warp 8          the schedule (it hands the items to the other warps through
 //                   a ring in shared memory), and keys and values: a ring of
 //                   tiles filled by TMA page by page
-//   warp 17         issues the products
-//   warps 18, 19    query rows of half A, B
+//   warp 9          issues the products
+//   warps 10, 11    query rows of half A, B
 // Scores S = Q K^T (tcgen05, both operands in shared memory) land in tensor
-// memory; the softmax threads read their row, and write the weights as 16-bit
+// memory; a softmax thread reads its row, and writes the weights as 16-bit
 // values over the scores, where the second product O += P V takes them as its
 // left operand: they never pass through shared memory.  512 columns of
 // tensor memory hold S/P and O of both halves.  The order of issue is
@@ -34,17 +34,16 @@ namespace attn {
 
 template <int DP>
 struct ChunkCfg {
-    static constexpr int kThreads = 640, kRows = 256, kTile = 128, kOv = 1;
+    static constexpr int kThreads = 384, kRows = 256, kTile = 128, kOv = 1;
     static constexpr uint32_t kQBytes = 128 * DP * 2;      // one half
     static constexpr uint32_t kTileBytes = 128 * DP * 2;   // keys or values of one tile
     static constexpr int kStages = DP == 128 ? 5 : 8;
     static constexpr uint32_t kRingOff = 2 * kQBytes;
     static constexpr uint32_t kBarOff = kRingOff + kStages * kTileBytes;
-    static constexpr uint32_t kMaxOff = kBarOff + 1024;    // [half][64-position part][row]: maxima, then sums
-    static constexpr uint32_t kBytes = kMaxOff + 2048;
+    static constexpr uint32_t kBytes = kBarOff + 1024 + 1024;   // + alignment slack
     static constexpr int kSlotFloats = kRows * DP + 2 * kRows;
     static constexpr uint32_t kOCol = 256;                 // O_A, O_B at 256 + DP * half; S at 128 * half
-    static constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;   // 4 * 104 + 64 = 5 * 96, the launch's share
+    static constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;   // 2 * 200 + 104 = 3 * 168, the launch's share
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -153,7 +152,7 @@ struct ChunkItem {
 
 struct ChunkBars {
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t s_full[2], p_ready[2], o_full[2], q_full[2], q_free[2];
+    uint64_t s_full[2], p_ready[2][2], o_full[2], q_full[2], q_free[2];   // p_ready: of either 64 positions of the tile
     uint64_t item_full[4], item_empty[4];
     uint64_t tail, drain;
     uint32_t tmem;
@@ -161,6 +160,14 @@ struct ChunkBars {
     uint32_t bad[8];   // per tile (mod 8): bit i, positions 16 i ... + 15 are on no page of the cache
     ChunkItem item[4];
 };
+
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 
 // Bits 0 ... n - 1 of a word (n of any size).
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
@@ -184,23 +191,20 @@ __device__ __forceinline__ bool chunk_wait(uint64_t *bar, uint32_t parity, Chunk
 }
 
 template <int DP, bool F16>
-__global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ AttnParams p)
 {
     using C = ChunkCfg<DP>;
     using W = Walker<C::kThreads, C::kRows, C::kTile, C::kOv>;
     using namespace sm100;
     constexpr int ST = C::kStages;
-    extern __shared__ __align__(1024) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     ChunkBars *bars = reinterpret_cast<ChunkBars *>(smem + C::kBarOff);
     static_assert(sizeof(ChunkBars) <= 1024, "barriers and items fit their place");
     int64_t *pre = reinterpret_cast<int64_t *>(smem + C::kRingOff);   // before the ring is used
     const BatchView &v = p.v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (smem_u32(smem) & 1023u) {   // the swizzled tiles need this; all of the memory is used, so none is left to align with
-        if (threadIdx.x == 0) atomicExch(p.err, 1);
-        return;
-    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; s++) {
             mbar_init(&bars->kv_full[s], 1);
@@ -208,14 +212,14 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
         }
         for (int h = 0; h < 2; h++) {
             mbar_init(&bars->s_full[h], 1);
-            mbar_init(&bars->p_ready[h], 8);
+            for (int i = 0; i < 2; i++) mbar_init(&bars->p_ready[h][i], 4);
             mbar_init(&bars->o_full[h], 1);
             mbar_init(&bars->q_full[h], 1);
             mbar_init(&bars->q_free[h], 1);
         }
         for (int i = 0; i < 4; i++) {
             mbar_init(&bars->item_full[i], 1);
-            mbar_init(&bars->item_empty[i], 19);   // 16 softmax warps, the products, 2 warps of query rows
+            mbar_init(&bars->item_empty[i], 11);   // 8 softmax warps, the products, 2 warps of query rows
         }
         mbar_init(&bars->tail, 1);
         mbar_init(&bars->drain, 1);
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
         tma_prefetch_desc(&p.tk);
         tma_prefetch_desc(&p.tv);
     }
-    if (warp == 17) {
+    if (warp == 9) {
         tmem_alloc(&bars->tmem, 512);
         tmem_relinquish();
     }
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
     if (threadIdx.x == 0) p.desc[cta].parts = 0;
     const uint32_t tmem = bars->tmem;
     W walk;
-    if (warp == 16) {
+    if (warp == 8) {
         walk.init(v, pre, cta < G ? cta * total / G : 0, cta < G ? (cta + 1) * total / G : 0, p.whole_items);
         fence_proxy_async_smem();
     }
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
     // The n-th item of this CTA, or null at the end or after a failure.
     auto item_at = [&](uint32_t n) -> const ChunkItem * {
         bool ok = chunk_wait(&bars->item_full[n & 3], (n >> 2) & 1, bars, p);
-        if (warp != 17) ok = __all_sync(0xffffffffu, ok);   // the products' warp runs one thread
+        if (warp != 9) ok = __all_sync(0xffffffffu, ok);   // the products' warp runs one thread
         if (!ok) return nullptr;
         const ChunkItem *it = &bars->item[n & 3];
         return it->h < 0 ? nullptr : it;
@@ -258,9 +262,9 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
         return (int64_t)(it->q0 + g / v.group) * v.heads + it->h * v.group + g % v.group;
     };
 
-    if (warp >= 16) {
+    if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-        if (warp == 16) {
+        if (warp == 8) {
             // ---- schedule; keys and values, in the order K(0) V(0) K(1) V(1) ... ----
             const int box = min(1 << v.page_shift, 128), pieces = 128 / box;
             uint32_t n = 0, tiles = 0, tails = 0, items = 0;   // ring entries, tiles, tail waits, items so far
@@ -351,9 +355,11 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
                     mbar_wait_bounded(&bars->kv_full[j % ST], (j / ST) & 1, p.timeout_ns / 8);
                 mbar_wait_bounded(&bars->tail, tails & 1, p.timeout_ns / 8);
             }
-        } else if (warp == 17) {
+        } else if (warp == 9) {
             // ---- products ----
-            if (lane == 0) {
+            // (elect.sync, not lane == 0: the compiler then keeps the products' operands in uniform
+            // registers; with a lane's branch each product took 130 cycles to issue)
+            if (elect_one()) {
                 const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0, F16), idesc_o = idesc_bf16_f32(128, DP, 0, 1, F16);
                 const uint64_t qd = smem_desc_sw128(smem_u32(smem), 16, 1024),
                                kd = smem_desc_sw128(smem_u32(smem + C::kRingOff), 16, 1024),
@@ -410,14 +416,17 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
                 };
                 auto values = [&](int h, int t, uint32_t slot) {
                     if (t < pr[h].first || t > pr[h].last) return;
-                    wait(&bars->p_ready[h], (n_p >> h) & 1);
-                    n_p ^= 1u << h;
-                    if (!ok) return;
                     const uint32_t d = tmem + C::kOCol + DP * h, a = tmem + 128 * h,
                                    v_lo = v_desc + slot * (C::kTileBytes >> 4);
-                    tc_mma_ts(d, a, v_lo, hi, idesc_o, t > pr[h].first);
 #pragma unroll
-                    for (int kk = 1; kk < 8; kk++) tc_mma_ts(d, a + 8 * kk, v_lo + (2048 >> 4) * kk, hi, idesc_o, 1);
+                    for (int i = 0; i < 2; i++) {
+                        wait(&bars->p_ready[h][i], (n_p >> h) & 1);
+                        if (!ok) return;
+#pragma unroll
+                        for (int kk = 4 * i; kk < 4 * i + 4; kk++)
+                            tc_mma_ts(d, a + 8 * kk, v_lo + (2048 >> 4) * kk, hi, idesc_o, kk > 0 || t > pr[h].first);
+                    }
+                    n_p ^= 1u << h;
                     if (t == pr[h].last) tc_commit(&bars->o_full[h]);
                 };
                 uint32_t slot = 0, phase = 0;   // of the next ring entry
@@ -473,7 +482,7 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
             }
         } else {
             // ---- query rows of one half ----
-            const int h = warp - 18;
+            const int h = warp - 10;
             uint8_t *dst = smem + h * C::kQBytes;
             uint32_t n = 0, items = 0;
             bool ok = true;
@@ -519,19 +528,9 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         // ---- softmax and epilogue of one half ----
-        // Warps w and w + 4 of a half share rows: w takes positions 0-63 of a tile, w + 4 the rest.
-        const int h = warp >> 3, part = (warp >> 2) & 1, row = threadIdx.x & 127;
+        const int h = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t s_addr = tmem + lanes + 128 * h, o_addr = tmem + lanes + C::kOCol + DP * h + (DP / 2) * part;
-        float *mine = reinterpret_cast<float *>(smem + C::kMaxOff) + (h * 2 + part) * 128 + row;
-        const float *other = reinterpret_cast<const float *>(smem + C::kMaxOff) + (h * 2 + (part ^ 1)) * 128 + row;
-        const int pair_bar = 1 + h * 4 + (warp & 3);
-        // The two warps meet at a barrier without a time limit, so neither may leave the other
-        // there: a warp that gives up arrives once more, and each looks for a failure before
-        // every meeting.  The arrival comes after the failure is marked, so a warp that met
-        // it sees the mark before the next meeting.
-        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
-        auto failed = [&]() { return __any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&bars->abort)) != 0; };
+        const uint32_t s_addr = tmem + lanes + 128 * h, o_addr = tmem + lanes + C::kOCol + DP * h;
         uint32_t n_s = 0, n_o = 0, tiles = 0;
         bool ok = true;
         const ChunkItem *it;
@@ -539,28 +538,26 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
             const Half f = it->half[h];
             const bool valid = row < f.rows, has = f.has();
             const int pos = valid ? it->pos0 + (it->row0 + h * 128 + row) / v.group : -1;
-            const int t_end = it->t1, t_begin = it->t0;
             float m = -INFINITY, l = 0.0f;   // m: the maximum that the weights are taken against
-            for (int t = t_begin; t < t_end; t++, tiles++) {
-                if (!f.takes(t)) continue;
-                const int tok0 = it->tiles.at(t) * 128 + 64 * part;
-                ok = chunk_wait(&bars->s_full[h], n_s & 1, bars, p);
-                ok = __all_sync(0xffffffffu, ok && !*reinterpret_cast<volatile int *>(&bars->abort));
+            for (int t = f.t_first; t <= f.t_last; t++) {
+                const int tok0 = it->tiles.at(t) * 128;
+                ok = chunk_wait(&bars->s_full[h], n_s, bars, p);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                n_s++;
+                n_s ^= 1;
                 tc_fence_after();
-                const uint32_t bad = (bars->bad[tiles & 7] >> (4 * part)) & 15u;
-                uint32_t s[2][32];
+                uint32_t s[4][32];
 #pragma unroll
-                for (int c = 0; c < 2; c++) tmem_ld_32x32b_x32(s_addr + 64 * part + 32 * c, s[c]);
+                for (int c = 0; c < 4; c++) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);
+                const uint32_t bad = bars->bad[(tiles + t - it->t0) & 7];
+                const bool all_seen = tok0 + 127 <= f.first && bad == 0 &&
+                                      (v.window <= 0 || tok0 > f.last - v.window || tok0 + 127 < v.sinks);
                 tmem_ld_wait();
-                const bool all_seen = tok0 + 63 <= f.first && bad == 0 &&
-                                      (v.window <= 0 || tok0 > f.last - v.window || tok0 + 63 < v.sinks);
                 if (!all_seen) {
                     // columns [0, up) are not after the row; of them [0, front) are sinks and [low, up) in the window
                     const int up = pos - tok0 + 1, low = v.window > 0 ? pos - v.window + 1 - tok0 : 0, front = v.sinks - tok0;
 #pragma unroll
-                    for (int g = 0; g < 2; g++) {
+                    for (int g = 0; g < 4; g++) {
                         uint32_t seen = bits_below(up - 32 * g) & (~bits_below(low - 32 * g) | bits_below(front - 32 * g));
                         if ((bad >> (2 * g)) & 1u) seen &= 0xffff0000u;
                         if ((bad >> (2 * g + 1)) & 1u) seen &= 0x0000ffffu;
@@ -571,14 +568,11 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
                 }
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 32; c++) x[c & 3] = max3(x[c & 3], __uint_as_float(s[0][c]), __uint_as_float(s[1][c]));
-                float top = fmaxf(max3(x[0], x[1], x[2]), x[3]);
-                // the other thread's maximum of the row.  (Its next write waits for S of the next
-                // tile, so for the weights of this one, so for this read.)  The barrier also says
-                // that both have their scores in registers: the weights overwrite them.
-                *mine = top;
-                pair_sync();
-                top = fmaxf(top, *other) * p.scale_log2;
+                for (int c = 0; c < 32; c++) {
+                    x[c & 1] = max3(x[c & 1], __uint_as_float(s[0][c]), __uint_as_float(s[1][c]));
+                    x[2 + (c & 1)] = max3(x[2 + (c & 1)], __uint_as_float(s[2][c]), __uint_as_float(s[3][c]));
+                }
+                const float top = fmaxf(max3(x[0], x[1], x[2]), x[3]) * p.scale_log2;
                 if (t == f.t_first) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, top > m + 8.0f)) {
@@ -587,7 +581,7 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
                     m = nm;
                     l *= fac;
 #pragma unroll 1
-                    for (int c = 0; c < DP / 32; c++) {
+                    for (int c = 0; c < DP / 16; c++) {
                         uint32_t o[16];
                         tmem_ld_x16(o_addr + 16 * c, o);
                         tmem_ld_wait();
@@ -596,46 +590,45 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
                         tmem_st_x16(o_addr + 16 * c, o);
                     }
                 }
-                const float u = m == -INFINITY ? 0.0f : m;
+                const float shift = m == -INFINITY ? 0.0f : -m;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int g = 0; g < 2; g++) {
+                for (int g = 0; g < 4; g++) {
                     uint32_t w[16];
 #pragma unroll
                     for (int c = 0; c < 16; c++) {
-                        const float a = ex2(__fmaf_rn(__uint_as_float(s[g][2 * c]), p.scale_log2, -u));
-                        const float b = ex2(__fmaf_rn(__uint_as_float(s[g][2 * c + 1]), p.scale_log2, -u));
+                        const float a = ex2(__fmaf_rn(__uint_as_float(s[g][2 * c]), p.scale_log2, shift));
+                        const float b = ex2(__fmaf_rn(__uint_as_float(s[g][2 * c + 1]), p.scale_log2, shift));
                         sum[(2 * c) & 3] += a;
                         sum[(2 * c + 1) & 3] += b;
                         w[c] = pack2<F16>(a, b);
                     }
-                    tmem_st_x16(s_addr + 32 * part + 16 * g, w);
+                    tmem_st_x16(s_addr + 16 * g, w);
+                    if (g & 1) {   // the second product begins with the first 64 positions
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->p_ready[h][g >> 1]);
+                    }
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_ready[h]);
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
             if (!ok) break;
-            // ---- epilogue: this thread's half of the row's columns ----
+            // ---- epilogue ----
             const bool whole = it->whole;
             const int slot = 2 * (int)cta + (items == 0 ? 0 : 1), pr = h * 128 + row;
-            float *out_part = p.part + (int64_t)slot * C::kSlotFloats;
+            float *part = p.part + (int64_t)slot * C::kSlotFloats;
             const int64_t orow = valid ? tensor_row(it, pr) : 0;
-            if (has) {   // complete: so the other thread is done with the last tile's maximum
-                ok = chunk_wait(&bars->o_full[h], n_o & 1, bars, p);
+            const float inv = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+            if (has) {
+                ok = chunk_wait(&bars->o_full[h], n_o, bars, p);
                 ok = __all_sync(0xffffffffu, ok);
-                n_o++;
+                if (!ok) break;
+                n_o ^= 1;
                 tc_fence_after();
             }
-            if (!ok || !(ok = !failed())) break;
-            *mine = l;
-            pair_sync();
-            l += *other;
-            const float inv = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
 #pragma unroll 1
-            for (int c = 0; c < DP / 64; c++) {
+            for (int c = 0; c < DP / 32; c++) {
                 uint32_t o[32];
                 if (has) {
                     tmem_ld_32x32b_x32(o_addr + 32 * c, o);
@@ -645,13 +638,13 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
                     for (int i = 0; i < 32; i++) o[i] = 0u;
                 }
                 if (!valid) continue;
-                const int col = (DP / 2) * part + 32 * c;
                 if (whole) {
-                    const int64_t at = orow * v.head_dim + col;
+                    const int64_t at = orow * v.head_dim + 32 * c;
                     uint16_t *dst = static_cast<uint16_t *>(p.out) + at;
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        if (col + 8 * i >= v.head_dim || !QLORA_IN(at + 8 * i + 7, (int64_t)v.tokens * v.heads * v.head_dim))
+                        if (32 * c + 8 * i >= v.head_dim ||
+                            !QLORA_IN(at + 8 * i + 7, (int64_t)v.tokens * v.heads * v.head_dim))
                             break;
                         uint32_t w[4];
 #pragma unroll
@@ -662,29 +655,26 @@ __global__ void __launch_bounds__(640, 1) chunk_kernel(const __grid_constant__ A
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; i++)
-                        *reinterpret_cast<uint4 *>(out_part + pr * DP + col + 4 * i) =
+                        *reinterpret_cast<uint4 *>(part + pr * DP + 32 * c + 4 * i) =
                             make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
             }
-            if (valid && part == 0) {
-                if (!whole) {
-                    out_part[C::kRows * DP + pr] = m;
-                    out_part[C::kRows * DP + C::kRows + pr] = l;
-                } else if (p.lse) {
-                    p.lse[orow] = l > 0.0f ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
-                }
+            if (valid && !whole) {
+                part[C::kRows * DP + pr] = m;
+                part[C::kRows * DP + C::kRows + pr] = l;
+            } else if (valid && p.lse) {
+                p.lse[orow] = l > 0.0f ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
             }
             if (it->begins && threadIdx.x == 0) p.desc[cta] = Desc{it->b, it->h, it->rt, slot, (int)cta, it->parts};
+            tiles += it->t1 - it->t0;
             tc_fence_before();   // these reads of O come before the next item's first product, behind p_ready
-            if (!(ok = !failed())) break;
-            pair_sync();         // the sums have been read: the next maxima may take their place
+            __syncwarp();
             if (lane == 0) mbar_arrive(&bars->item_empty[items & 3]);
         }
-        if (failed()) asm volatile("bar.arrive %0, 64;" ::"r"(pair_bar) : "memory");
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 17) {
+    if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
