@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     }
     if (row >= rows) return;
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    const int g = d.rt * ROWS + row0 + row;
-    const int64_t orow = (int64_t)(r.q0 + g / v.group) * v.heads + d.h * v.group + g % v.group;
+    const int g = d.rt * ROWS + row0 + row, tok = v.token_of(g);
+    const int64_t orow = (int64_t)(r.q0 + tok) * v.heads + d.h * v.group + g - tok * v.group;
     const int64_t at = orow * v.head_dim + lane * V;
     if (lane * V < v.head_dim && QLORA_IN(at + V - 1, (int64_t)v.tokens * v.heads * v.head_dim)) {
         uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + at);
@@ -80,7 +80,71 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     if (lane == 0 && p.lse) p.lse[orow] = L > 0.0f ? (M + log2f(L)) * 0.69314718056f : -INFINITY;
 }
 
+// The same for the items of the kernel of many rows: block y takes 32 rows, one
+// per lane; its warps divide the columns, which the parts hold four by four for
+// all rows.  The joined rows pass through shared memory, so that they leave
+// as whole lines.
+template <int DP, bool F16>
+__global__ void __launch_bounds__(256) combine_rows_kernel(const __grid_constant__ AttnParams p)
+{
+    constexpr int ROWS = ChunkCfg<DP>::kRows;
+    __shared__ uint2 rows_out[32][DP / 4 + 1];
+    sm100::pdl_wait();
+    sm100::pdl_trigger();
+    const BatchView &v = p.v;
+    const Desc d = p.desc[blockIdx.x];
+    if (d.parts == 0) return;
+    const Request r = load_request(v, d.b);
+    const int row0 = blockIdx.y * 32, rows = min(min(r.qn * v.group - d.rt * ROWS, ROWS) - row0, 32);
+    if (rows <= 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int64_t kSlot = ChunkCfg<DP>::kSlotFloats;
+    auto slot = [&](int i) { return p.part + (i == 0 ? d.first_slot : 2 * (d.cta + i)) * kSlot; };
+    auto tensor_row = [&](int row) {
+        const int g = d.rt * ROWS + row0 + row, t = v.token_of(g);
+        return (int64_t)(r.q0 + t) * v.heads + d.h * v.group + g - t * v.group;
+    };
+    if (lane < rows) {
+        float M = -INFINITY, L = 0.0f;
+        for (int i = 0; i < d.parts; i++) M = fmaxf(M, slot(i)[ROWS * DP + row0 + lane]);
+        float4 a[DP / 32];
+#pragma unroll
+        for (int k = 0; k < DP / 32; k++) a[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+        for (int i = 0; i < d.parts; i++) {
+            const float *s = slot(i) + row0 + lane;
+            const float m = s[ROWS * DP], f = m == -INFINITY ? 0.0f : exp2f(m - M);
+            L += f * s[ROWS * DP + ROWS];
+#pragma unroll
+            for (int k = 0; k < DP / 32; k++) {
+                const float4 x = *reinterpret_cast<const float4 *>(slot(i) + ((8 * k + warp) * ROWS + row0 + lane) * 4);
+                a[k].x += f * x.x;
+                a[k].y += f * x.y;
+                a[k].z += f * x.z;
+                a[k].w += f * x.w;
+            }
+        }
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll
+        for (int k = 0; k < DP / 32; k++)
+            rows_out[lane][8 * k + warp] = make_uint2(pack2<F16>(a[k].x * inv, a[k].y * inv), pack2<F16>(a[k].z * inv, a[k].w * inv));
+        if (warp == 0 && p.lse) p.lse[tensor_row(lane)] = L > 0.0f ? (M + log2f(L)) * 0.69314718056f : -INFINITY;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (DP / 4); i += 256) {
+        const int row = i / (DP / 4), c = i % (DP / 4);
+        const int64_t at = tensor_row(row) * v.head_dim + 4 * c;
+        if (4 * c < v.head_dim && QLORA_IN(at + 3, (int64_t)v.tokens * v.heads * v.head_dim))
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = rows_out[row][c];
+    }
+}
+
 namespace {
+
+int log2_of(int32_t n)   // -1 if n is no power of two
+{
+    return n & (n - 1) ? -1 : page_shift(n);
+}
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -127,7 +191,7 @@ qlora_status launch_chunk(AttnParams &p, const DeviceInfo &dev, cudaStream_t s)
     }
     {
         LaunchScope ls(QLORA_KERNEL_ATTENTION, s);
-        QLORA_CUDA_TRY(launch_pdl(combine_kernel<C::kRows, DP, F16>, dim3(dev.sms, C::kRows / 8), dim3(256), 0, s, p));
+        QLORA_CUDA_TRY(launch_pdl(combine_rows_kernel<DP, F16>, dim3(dev.sms, C::kRows / 32), dim3(256), 0, s, p));
     }
     return launch_status();
 }
@@ -192,8 +256,9 @@ extern "C" qlora_status qlora_paged_attn_fwd(const qlora_kv_cache *cache, const 
     QLORA_TRY(make_cache_map(&p.tk, cache, cache->k, box));
     QLORA_TRY(make_cache_map(&p.tv, cache, cache->v, box));
     p.v = BatchView{kv->cu_q, kv->kv_len, kv->block_table, kv->batch, kv->max_pages, kv->tokens, cache->num_pages,
-                    page_shift(cache->page_size), heads, cache->kv_heads, heads / cache->kv_heads, cache->head_dim,
-                    window >= kMaxPositions ? 0 : window, std::min(sinks, (int32_t)kMaxPositions)};
+                    log2_of(cache->page_size), heads, cache->kv_heads, heads / cache->kv_heads, cache->head_dim,
+                    window >= kMaxPositions ? 0 : window, std::min(sinks, (int32_t)kMaxPositions),
+                    log2_of(heads / cache->kv_heads)};
     p.q = q;
     p.out = out;
     p.lse = lse;

@@ -20,10 +20,14 @@
 // products.  Products of one CTA complete in order: the completion of S(j + 1)
 // tells the softmax that PV(j) is done too.
 //
-// Softmax: one pass, and the output is rescaled only when a row's maximum has
-// grown by more than 2^8 since its last rescaling (weights stay below 2^8, sums
-// and outputs are exact in scale); rescaling is then done by the softmax
-// threads, between S(j) and the weights of j.  The weights are rounded to the
+// Softmax: one pass, with weights against a reference m that is the row's maximum
+// over its first tile and moves only when it has to.  Any reference gives the same
+// quotient as long as no weight leaves the 16-bit type's range, and the sum
+// of a tile's weights, which is needed anyway, tells: up to 2^15 none has.  So the
+// maximum of a tile is not looked for at all, unless that sum is larger or the row
+// has had no reference yet; then the weights are formed again against the new
+// maximum, and the output is rescaled by the softmax threads before they are
+// handed over.  The weights are rounded to the
 // operands' 16-bit type (half a step each, averaged over the keys: the output's
 // own rounding is as large); sums are taken of the unrounded fp32 weights.
 #pragma once
@@ -53,11 +57,30 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c)
+// Two floats in one 64-bit register, for the packed fp32 instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b)
 {
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t r)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // The products of this kernel.  Descriptors of one operand differ in the low
@@ -108,14 +131,20 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// One half of an item: its rows' positions, and the CTA's tiles that it takes:
-// from the first to the last that any of its rows sees.
+// The CTA's tiles that a half of an item takes: from the first to the last that
+// any of its rows sees, without those between its sinks and its window.
+struct Range {
+    int first, last;   // last < first: none
+    int gap, gap_end;  // [gap, gap_end) is left out
+
+    __device__ __forceinline__ bool has() const { return last >= first; }
+    __device__ __forceinline__ bool takes(int t) const { return t >= first && t <= last && (t < gap || t >= gap_end); }
+};
+
+// One half of an item: its rows' positions, and its tiles.
 struct Half {
     int rows, first, last;   // valid rows (0: none), position of the first and the last
-    int t_first, t_last;     // tiles; t_last < t_first: none
-
-    __device__ __forceinline__ bool has() const { return t_last >= t_first; }
-    __device__ __forceinline__ bool takes(int t) const { return t >= t_first && t <= t_last; }
+    Range t;
 };
 
 __device__ __forceinline__ Half half_of(const BatchView &v, const Item &it, int half)
@@ -123,17 +152,18 @@ __device__ __forceinline__ Half half_of(const BatchView &v, const Item &it, int 
     Half f;
     f.rows = min(max(it.r.qn * v.group - it.rt * 256 - half * 128, 0), 128);
     f.first = f.last = -1;
-    f.t_first = it.t0;
-    f.t_last = it.t0 - 1;
+    f.t = Range{it.t0, it.t0 - 1, 0, 0};
     if (f.rows == 0) return f;
     item_positions<128>(v, it.r, it.rt * 2 + half, f.first, f.last);
-    f.t_last = it.t1 - 1;
     auto sees = [&](int t) {
         const int a = it.tiles.at(t) * 128;
         return a <= f.last && (v.window <= 0 || a + 127 > f.first - v.window || a < v.sinks);
     };
-    while (f.t_last >= f.t_first && !sees(f.t_last)) f.t_last--;
-    while (f.t_last >= f.t_first && !sees(f.t_first)) f.t_first++;
+    f.t.last = it.t1 - 1;
+    while (f.t.has() && !sees(f.t.last)) f.t.last--;
+    while (f.t.has() && !sees(f.t.first)) f.t.first++;
+    f.t.gap = f.t.gap_end = max(f.t.first, it.tiles.sink_tiles);
+    while (f.t.gap_end <= f.t.last && !sees(f.t.gap_end)) f.t.gap_end++;
     return f;
 }
 
@@ -152,7 +182,7 @@ struct ChunkItem {
 
 struct ChunkBars {
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t s_full[2], p_ready[2][2], o_full[2], q_full[2], q_free[2];   // p_ready: of either 64 positions of the tile
+    uint64_t s_full[2], p_ready[2], o_full[2], q_full[2], q_free[2];
     uint64_t item_full[4], item_empty[4];
     uint64_t tail, drain;
     uint32_t tmem;
@@ -212,7 +242,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
         }
         for (int h = 0; h < 2; h++) {
             mbar_init(&bars->s_full[h], 1);
-            for (int i = 0; i < 2; i++) mbar_init(&bars->p_ready[h][i], 4);
+            mbar_init(&bars->p_ready[h], 4);
             mbar_init(&bars->o_full[h], 1);
             mbar_init(&bars->q_full[h], 1);
             mbar_init(&bars->q_free[h], 1);
@@ -258,8 +288,8 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
     };
     // The row of q, out and lse (times heads, plus the head) of an item's row.
     auto tensor_row = [&](const ChunkItem *it, int r) {
-        const int g = it->row0 + r;
-        return (int64_t)(it->q0 + g / v.group) * v.heads + it->h * v.group + g % v.group;
+        const int g = it->row0 + r, t = v.token_of(g);
+        return (int64_t)(it->q0 + t) * v.heads + it->h * v.group + g - t * v.group;
     };
 
     if (warp >= 8) {
@@ -374,10 +404,9 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 // S runs one tile ahead of PV, across items.  The thread keeps what it needs of
                 // both tiles' items in registers: what it does between two products is
                 // latency that nothing hides.
-                struct Range {
-                    int first, last;
-                };
-                Range sr[2] = {}, pr[2] = {};
+                Range sr[2] = {};
+                // for each half (4 h + ...): 1 it takes the tile, 2 as its first of the item, 4 as its last
+                uint32_t s_how = 0;
                 bool more = true, crossed = false;   // is there a tile for S; is it of another item than PV's
                 uint32_t items = 0;                  // items begun
                 int st = -1, s_end = 0;
@@ -393,12 +422,17 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                         st = it->t0;
                         s_end = it->t1;
 #pragma unroll
-                        for (int h = 0; h < 2; h++) sr[h] = Range{it->half[h].t_first, it->half[h].t_last};
+                        for (int h = 0; h < 2; h++) sr[h] = it->half[h].t;
                     }
+                    s_how = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; h++)
+                        if (sr[h].takes(st)) s_how |= (1u | (st == sr[h].first ? 2u : 0u) | (st == sr[h].last ? 4u : 0u)) << (4 * h);
                 };
                 auto scores = [&](int h, uint32_t slot) {
-                    if (st < sr[h].first || st > sr[h].last) return;
-                    if (st == sr[h].first) {
+                    const uint32_t how = s_how >> (4 * h);
+                    if (!(how & 1u)) return;
+                    if (how & 2u) {
                         wait(&bars->q_full[h], (n_q >> h) & 1);
                         n_q ^= 1u << h;
                     }
@@ -412,22 +446,20 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                         tc_mma_ss<true>(d, q_lo + o, k_lo + o, hi, idesc_s);
                     }
                     tc_commit(&bars->s_full[h]);
-                    if (st == sr[h].last) tc_commit(&bars->q_free[h]);
+                    if (how & 4u) tc_commit(&bars->q_free[h]);
                 };
-                auto values = [&](int h, int t, uint32_t slot) {
-                    if (t < pr[h].first || t > pr[h].last) return;
+                auto values = [&](int h, uint32_t hows, uint32_t slot) {
+                    const uint32_t how = hows >> (4 * h);
+                    if (!(how & 1u)) return;
                     const uint32_t d = tmem + C::kOCol + DP * h, a = tmem + 128 * h,
                                    v_lo = v_desc + slot * (C::kTileBytes >> 4);
+                    wait(&bars->p_ready[h], (n_p >> h) & 1);
+                    if (!ok) return;
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        wait(&bars->p_ready[h][i], (n_p >> h) & 1);
-                        if (!ok) return;
-#pragma unroll
-                        for (int kk = 4 * i; kk < 4 * i + 4; kk++)
-                            tc_mma_ts(d, a + 8 * kk, v_lo + (2048 >> 4) * kk, hi, idesc_o, kk > 0 || t > pr[h].first);
-                    }
+                    for (int kk = 0; kk < 8; kk++)
+                        tc_mma_ts(d, a + 8 * kk, v_lo + (2048 >> 4) * kk, hi, idesc_o, kk > 0 || !(how & 2u));
                     n_p ^= 1u << h;
-                    if (t == pr[h].last) tc_commit(&bars->o_full[h]);
+                    if (how & 4u) tc_commit(&bars->o_full[h]);
                 };
                 uint32_t slot = 0, phase = 0;   // of the next ring entry
                 auto advance = [&]() {
@@ -448,23 +480,21 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 }
                 while (more && ok) {
                     // PV of this tile, S of the next
-                    const int t = st;
-                    pr[0] = sr[0];
-                    pr[1] = sr[1];
+                    const uint32_t p_how = s_how;
                     next_tile();
                     const uint32_t vs = advance();
                     if (!crossed) {
                         const uint32_t ks = advance();
-                        values(0, t, vs);
+                        values(0, p_how, vs);
                         if (ok) scores(0, ks);
-                        if (ok) values(1, t, vs);
+                        if (ok) values(1, p_how, vs);
                         if (!ok) break;
                         tc_commit(&bars->kv_empty[vs]);
                         scores(1, ks);
                         if (ok) tc_commit(&bars->kv_empty[ks]);
                     } else {   // the next item's query rows may still be on their way
-                        if (ok) values(0, t, vs);
-                        if (ok) values(1, t, vs);
+                        if (ok) values(0, p_how, vs);
+                        if (ok) values(1, p_how, vs);
                         if (!ok) break;
                         tc_commit(&bars->kv_empty[vs]);
                         if (!more) break;
@@ -488,7 +518,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
             bool ok = true;
             for (const ChunkItem *it; ok && (it = item_at(items)); items++) {
                 const Half f = it->half[h];
-                if (f.has()) {
+                if (f.t.has()) {
                     if (n > 0) ok = chunk_wait(&bars->q_free[h], (n - 1) & 1, bars, p);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -520,7 +550,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    if (f.has()) mbar_arrive(&bars->q_full[h]);
+                    if (f.t.has()) mbar_arrive(&bars->q_full[h]);
                     mbar_arrive(&bars->item_empty[items & 3]);
                 }
             }
@@ -535,12 +565,15 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
         bool ok = true;
         const ChunkItem *it;
         for (uint32_t items = 0; ok && (it = item_at(items)); items++) {
-            const Half f = it->half[h];
-            const bool valid = row < f.rows, has = f.has();
-            const int pos = valid ? it->pos0 + (it->row0 + h * 128 + row) / v.group : -1;
-            float m = -INFINITY, l = 0.0f;   // m: the maximum that the weights are taken against
-            for (int t = f.t_first; t <= f.t_last; t++) {
+            const Half &f = it->half[h];
+            const int t_first = f.t.first, t_last = f.t.last;
+            const bool valid = row < f.rows, has = f.t.has();
+            const int pos = valid ? it->pos0 + v.token_of(it->row0 + h * 128 + row) : -1;
+            float m = valid ? -INFINITY : 0.0f, l = 0.0f;   // m: the reference of the weights, -inf: none yet
+            for (int t = t_first; t <= t_last; t++) {
+                if (!f.t.takes(t)) continue;
                 const int tok0 = it->tiles.at(t) * 128;
+                const bool inside = tok0 + 127 <= f.first && (v.window <= 0 || tok0 > f.last - v.window || tok0 + 127 < v.sinks);
                 ok = chunk_wait(&bars->s_full[h], n_s, bars, p);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -550,8 +583,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
 #pragma unroll
                 for (int c = 0; c < 4; c++) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);
                 const uint32_t bad = bars->bad[(tiles + t - it->t0) & 7];
-                const bool all_seen = tok0 + 127 <= f.first && bad == 0 &&
-                                      (v.window <= 0 || tok0 > f.last - v.window || tok0 + 127 < v.sinks);
+                const bool all_seen = inside && bad == 0;
                 tmem_ld_wait();
                 if (!all_seen) {
                     // columns [0, up) are not after the row; of them [0, front) are sinks and [low, up) in the window
@@ -566,52 +598,58 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                             if (!((seen >> c) & 1u)) s[g][c] = 0xff800000u;
                     }
                 }
-                float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float sum;
+                auto weights = [&]() {
+                    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), shift2 = pair(-m, -m);
+                    uint64_t sums[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 32; c++) {
-                    x[c & 1] = max3(x[c & 1], __uint_as_float(s[0][c]), __uint_as_float(s[1][c]));
-                    x[2 + (c & 1)] = max3(x[2 + (c & 1)], __uint_as_float(s[2][c]), __uint_as_float(s[3][c]));
+                    for (int g = 0; g < 4; g++) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int c = 0; c < 16; c++) {
+                            const float2 e = unpair(fma2(pair(__uint_as_float(s[g][2 * c]), __uint_as_float(s[g][2 * c + 1])), scale2, shift2));
+                            const float a = ex2(e.x), b = ex2(e.y);
+                            sums[c & 1] = add2(sums[c & 1], pair(a, b));
+                            w[c] = pack2<F16>(a, b);
+                        }
+                        tmem_st_x16(s_addr + 16 * g, w);
+                    }
+                    const float2 total = unpair(add2(sums[0], sums[1]));
+                    sum = total.x + total.y;
+                };
+                bool again = t == t_first;
+                if (!again) {
+                    weights();
+                    again = !(sum <= 32768.0f) || m == -INFINITY;
                 }
-                const float top = fmaxf(max3(x[0], x[1], x[2]), x[3]) * p.scale_log2;
-                if (t == f.t_first) {
-                    m = top;
-                } else if (__any_sync(0xffffffffu, top > m + 8.0f)) {
-                    // the product of the tile before is complete (this S came after it)
-                    const float nm = fmaxf(m, top), fac = nm == -INFINITY ? 1.0f : ex2(m - nm);
-                    m = nm;
-                    l *= fac;
+                if (__any_sync(0xffffffffu, again)) {
+                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 128; c++) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c >> 5][c & 31]));
+                    const float nm = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2);
+                    if (t > t_first) {
+                        // the product of the tile before is complete (this S came after it)
+                        const float fac = nm == -INFINITY ? 1.0f : ex2(m - nm);
+                        l *= fac;
 #pragma unroll 1
-                    for (int c = 0; c < DP / 16; c++) {
-                        uint32_t o[16];
-                        tmem_ld_x16(o_addr + 16 * c, o);
-                        tmem_ld_wait();
+                        for (int c = 0; c < DP / 16; c++) {
+                            uint32_t o[16];
+                            tmem_ld_x16(o_addr + 16 * c, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
-                        tmem_st_x16(o_addr + 16 * c, o);
+                            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
+                            tmem_st_x16(o_addr + 16 * c, o);
+                        }
                     }
+                    m = nm == -INFINITY ? 0.0f : nm;   // against 0, all weights of a row without a key are 0
+                    weights();
+                    m = nm;
                 }
-                const float shift = m == -INFINITY ? 0.0f : -m;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int c = 0; c < 16; c++) {
-                        const float a = ex2(__fmaf_rn(__uint_as_float(s[g][2 * c]), p.scale_log2, shift));
-                        const float b = ex2(__fmaf_rn(__uint_as_float(s[g][2 * c + 1]), p.scale_log2, shift));
-                        sum[(2 * c) & 3] += a;
-                        sum[(2 * c + 1) & 3] += b;
-                        w[c] = pack2<F16>(a, b);
-                    }
-                    tmem_st_x16(s_addr + 16 * g, w);
-                    if (g & 1) {   // the second product begins with the first 64 positions
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars->p_ready[h][g >> 1]);
-                    }
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += sum;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_ready[h]);
             }
             if (!ok) break;
             // ---- epilogue ----
@@ -655,7 +693,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; i++)
-                        *reinterpret_cast<uint4 *>(part + pr * DP + 32 * c + 4 * i) =
+                        *reinterpret_cast<uint4 *>(part + ((8 * c + i) * C::kRows + pr) * 4) =   // four columns of a row together
                             make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
             }

@@ -34,6 +34,9 @@ struct BatchView {
     int batch, max_pages, tokens, num_pages, page_shift;
     int heads, kv_heads, group, head_dim;
     int window, sinks;   // window 0: every earlier position is visible
+    int group_shift;     // group = 1 << group_shift, or -1
+
+    __device__ __forceinline__ int token_of(int row) const { return group_shift >= 0 ? row >> group_shift : row / group; }
 };
 
 // A CTA's partial results: at most two, of its first item (slot 2c) and of its
@@ -88,8 +91,8 @@ template <int ROWS>
 __device__ __forceinline__ void item_positions(const BatchView &v, const Request &r, int rt, int &first, int &last)
 {
     const int r0 = rt * ROWS, r1 = min(r.qn * v.group, r0 + ROWS) - 1;
-    first = r.kv - r.qn + r0 / v.group;
-    last = r.kv - r.qn + r1 / v.group;
+    first = r.kv - r.qn + v.token_of(r0);
+    last = r.kv - r.qn + v.token_of(r1);
 }
 
 template <int ROWS, int TILE>
@@ -143,8 +146,23 @@ __device__ __forceinline__ void schedule_scan(const BatchView &v, int64_t *pre)
     int64_t *warp_sum = pre + NT + 1;
     const int tid = threadIdx.x, lane = tid & 31, run = (v.batch + NT - 1) / NT;
     int64_t mine = 0;
-    for (int b = tid * run; b < min((tid + 1) * run, v.batch); b++)
-        mine += v.kv_heads * head_units<ROWS, TILE, OV>(v, load_request(v, b));
+    if (v.batch <= NT / 8) {   // few requests, maybe of many row tiles: a warp for each, its lanes take the tiles
+        for (int b = tid >> 5; b < v.batch; b += NT / 32) {
+            const Request r = load_request(v, b);
+            const int n = row_tiles<ROWS>(v, r);
+            int64_t u = 0;
+            for (int rt = lane; rt < n; rt += 32) u += max(item_tiles<ROWS, TILE>(v, r, rt).n, 1) + OV;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+            if (lane == 0) pre[b] = v.kv_heads * u;
+        }
+        __syncthreads();
+        if (tid < v.batch) mine = pre[tid];
+        __syncthreads();
+    } else {
+        for (int b = tid * run; b < min((tid + 1) * run, v.batch); b++)
+            mine += v.kv_heads * head_units<ROWS, TILE, OV>(v, load_request(v, b));
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -169,7 +187,6 @@ template <int NT, int ROWS, int TILE, int OV>
 struct Walker {
     int64_t u, u1;        // units still to take
     int64_t start;        // first unit of the current item
-    int64_t per_head;
     int b, h, rt, n_rt;
     Request r;
     bool whole_items;
@@ -185,39 +202,56 @@ struct Walker {
             const int mid = (lo + hi) >> 1;
             if (pre[mid] <= from) lo = mid; else hi = mid;
         }
-        // the request inside the run: 32 at a time, one per lane
         const int lane = threadIdx.x & 31, run = (v.batch + NT - 1) / NT;
-        const int b_end = min((lo + 1) * run, v.batch);
-        int64_t base = pre[lo];
-        for (int b0 = lo * run; b0 < b_end; b0 += 32) {
-            int64_t mine = 0;
-            if (b0 + lane < b_end) mine = v.kv_heads * head_units<ROWS, TILE, OV>(v, load_request(v, b0 + lane));
-            int64_t incl = mine;
+        int64_t per_head = 0;
+        if (run == 1) {
+            b = lo;
+            start = pre[lo];
+            per_head = (pre[lo + 1] - start) / v.kv_heads;
+        } else {   // the request inside the run: 32 at a time, one per lane
+            const int b_end = min((lo + 1) * run, v.batch);
+            int64_t base = pre[lo];
+            for (int b0 = lo * run; b0 < b_end; b0 += 32) {
+                int64_t mine = 0;
+                if (b0 + lane < b_end) mine = head_units<ROWS, TILE, OV>(v, load_request(v, b0 + lane));
+                int64_t incl = v.kv_heads * mine;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += up;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += up;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, base + incl > from);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    b = b0 + l;
+                    per_head = __shfl_sync(0xffffffffu, mine, l);
+                    start = base + __shfl_sync(0xffffffffu, incl, l) - v.kv_heads * per_head;
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, incl, 31);
             }
-            const unsigned past = __ballot_sync(0xffffffffu, base + incl > from);
-            if (past) {
-                const int l = __ffs(past) - 1;
-                b = b0 + l;
-                start = base + __shfl_sync(0xffffffffu, incl - mine, l);
-                break;
-            }
-            base += __shfl_sync(0xffffffffu, incl, 31);
         }
         r = load_request(v, b);
         n_rt = row_tiles<ROWS>(v, r);
-        per_head = head_units<ROWS, TILE, OV>(v, r);
         h = (int)((from - start) / per_head);
         start += h * per_head;
-        rt = 0;
-        for (;;) {
-            const int64_t c = max(item_tiles<ROWS, TILE>(v, r, rt).n, 1) + OV;
-            if (start + c > from) break;
-            start += c;
-            rt++;
+        for (rt = 0;; rt += 32) {   // the row tile: 32 at a time (past the last one: cost 0)
+            int incl = rt + lane < n_rt ? max(item_tiles<ROWS, TILE>(v, r, rt + lane).n, 1) + OV : 0;
+            const int mine = incl;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += up;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, start + incl > from);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                rt += l;
+                start += __shfl_sync(0xffffffffu, incl - mine, l);
+                break;
+            }
+            start += __shfl_sync(0xffffffffu, incl, 31);
+            if (rt + 32 >= n_rt) break;   // not reached: `from` lies inside the head
         }
         if (whole && start < from) {   // begins in the CTA before
             const int64_t c = max(item_tiles<ROWS, TILE>(v, r, rt).n, 1) + OV;
@@ -241,7 +275,6 @@ struct Walker {
             r = load_request(v, b);
             n_rt = row_tiles<ROWS>(v, r);
         } while (n_rt == 0);
-        per_head = 0;   // only init() divides by it
     }
 
     __device__ __forceinline__ bool next(const BatchView &v, Item &it)

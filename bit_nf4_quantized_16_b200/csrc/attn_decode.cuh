@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
         const int rows = min(it.r.qn * v.group - it.rt * C::kRows, C::kRows);
         const int pos0 = it.r.kv - it.r.qn;
         const int ra = lane >> 2, rb = ra + 8, gr0 = it.rt * C::kRows;
-        const int pos_a = ra < rows ? pos0 + (gr0 + ra) / v.group : -1;
-        const int pos_b = rb < rows ? pos0 + (gr0 + rb) / v.group : -1;
+        const int pos_a = ra < rows ? pos0 + v.token_of(gr0 + ra) : -1;
+        const int pos_b = rb < rows ? pos0 + v.token_of(gr0 + rb) : -1;
         int first, last;
         item_positions<C::kRows>(v, it.r, it.rt, first, last);
         // query rows as A operands: this lane's rows ra and rb
