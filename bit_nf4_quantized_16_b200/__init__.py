@@ -488,34 +488,34 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _is(t, dtype, shape, device, name):
-    """A dense tensor of this type and shape on this device."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+def _is(t, dtype, shape, index, name):
+    """The address of t: a dense tensor of this type and shape on device `index`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-class _On:
-    """Runs a call with `device` current and yields the raw stream."""
+def _on(index, stream, fn, args, where):
+    """fn(*args, raw stream) with device `index` current."""
+    if stream is None:
+        s = torch.cuda.current_stream(index).cuda_stream
+    else:
+        if stream.device.index != index:
+            raise ValueError(f"stream of {stream.device} for tensors on cuda:{index}")
+        s = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, s)
+    if status:
+        raise QLoraError(status, where)
 
-    __slots__ = ("stream", "index", "before")
 
-    def __init__(self, device, stream):
-        _need(device.type == "cuda", f"need tensors on a CUDA device, got {device}")
-        if stream is not None:
-            _need(stream.device == device, f"stream of {stream.device} for tensors on {device}")
-        self.index, self.before = device.index, torch.cuda.current_device()
-        self.stream = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-    def __enter__(self):
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _cuda_index(t):
+    _need(t.is_cuda, f"need tensors on a CUDA device, got {t.device}")
+    return t.get_device()
 
 
 class KVCache:
@@ -528,7 +528,7 @@ class KVCache:
               k.device == v.device, "k and v must be alike and have four dimensions")
         _need(k.stride(3) == 1 or k.shape[3] == 1, "the last dimension must be contiguous")
         _need(k.dtype in (torch.bfloat16, torch.float16), f"unsupported dtype {k.dtype}")
-        self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        self.k, self.v, self.device, self.dtype, self._index = k, v, k.device, k.dtype, _cuda_index(k)
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.desc = qlora_kv_cache(k.data_ptr(), v.data_ptr(), self.num_pages, self.page_size, self.kv_heads,
                                    self.head_dim, k.stride(0), k.stride(1), k.stride(2), _dtype_code(k))
@@ -550,15 +550,16 @@ class KVBatch:
         given = [t for t in (block_table, cu_q, kv_len, positions, slots) if t is not None]
         if device is None:
             device = given[0].device if given else "cuda"
-        self.device = device = torch.empty(0, device=device).device
+        probe = torch.empty(0, device=device)
+        self.device, self._index = probe.device, _cuda_index(probe)
         shapes = {"block_table": (batch, max_pages), "cu_q": (batch + 1,), "kv_len": (batch,), "positions": (tokens,),
                   "slots": (tokens,)}
         fill = {"block_table": -1, "positions": -1, "slots": -1}
         ptrs = []
         for (name, shape), t in zip(shapes.items(), (block_table, cu_q, kv_len, positions, slots)):
             if t is None:
-                t = torch.full(shape, fill.get(name, 0), dtype=torch.int32, device=device)
-            ptrs.append(_is(t, torch.int32, shape, device, name))
+                t = torch.full(shape, fill.get(name, 0), dtype=torch.int32, device=self.device)
+            ptrs.append(_is(t, torch.int32, shape, self._index, name))
             setattr(self, name, t)
         self.batch, self.max_pages, self.tokens, self.max_q_len = batch, max_pages, tokens, max_q_len
         self.desc = qlora_kv_batch(batch, max_pages, tokens, max_q_len, *ptrs)
@@ -574,31 +575,29 @@ def qlora_build_rope(head_dim: int, base: float = 10000.0) -> qlora_rope:
 def qlora_kv_plan(kv: KVBatch, page_size: int, num_pages: int, ctx_len, q_len, free_pages, free_count,
                   free_count_out=None, stream=None):
     """free_count_out: free_count itself (updated in place) if not given."""
-    i32, dev = torch.int32, kv.device
-    one = (1,)
-    out = free_count if free_count_out is None else free_count_out
-    args = (kv._ref, page_size, num_pages, _is(ctx_len, i32, (kv.batch,), dev, "ctx_len"),
-            _is(q_len, i32, (kv.batch,), dev, "q_len"), _is(free_pages, i32, (num_pages,), dev, "free_pages"),
-            _is(free_count, i32, one, dev, "free_count"), _is(out, i32, one, dev, "free_count_out"))
-    with _On(dev, stream) as s:
-        _check(lib.qlora_kv_plan(*args, s), "qlora_kv_plan")
+    i32, dev, batch = torch.int32, kv._index, (kv.batch,)
+    count = _is(free_count, i32, (1,), dev, "free_count")
+    out = count if free_count_out is None else _is(free_count_out, i32, (1,), dev, "free_count_out")
+    _on(dev, stream, lib.qlora_kv_plan,
+        (kv._ref, page_size, num_pages, _is(ctx_len, i32, batch, dev, "ctx_len"), _is(q_len, i32, batch, dev, "q_len"),
+         _is(free_pages, i32, (num_pages,), dev, "free_pages"), count, out), "qlora_kv_plan")
 
 
 def qlora_kv_append(cache: KVCache, kv: KVBatch, rope, q, k, v, q_out=None, stream=None):
     """q [tokens, heads, head_dim], k and v [tokens, kv_heads, head_dim]; q_out: q itself if not given."""
     _need(q.dim() == 3, "q: need [tokens, heads, head_dim]")
-    _need(cache.device == kv.device, "cache and batch on different devices")
-    T, H, D, dt, dev = kv.tokens, q.shape[1], cache.head_dim, cache.dtype, cache.device
+    _need(cache._index == kv._index, "cache and batch on different devices")
+    T, H, D, dt, dev = kv.tokens, q.shape[1], cache.head_dim, cache.dtype, cache._index
     new = (T, cache.kv_heads, D)
     qp = _is(q, dt, (T, H, D), dev, "q")
-    args = (cache._ref, kv._ref, None if rope is None else ctypes.addressof(rope), qp, _is(k, dt, new, dev, "k"),
-            _is(v, dt, new, dev, "v"), H, qp if q_out is None else _is(q_out, dt, (T, H, D), dev, "q_out"))
-    with _On(dev, stream) as s:
-        _check(lib.qlora_kv_append(*args, s), "qlora_kv_append")
+    _on(dev, stream, lib.qlora_kv_append,
+        (cache._ref, kv._ref, None if rope is None else ctypes.addressof(rope), qp, _is(k, dt, new, dev, "k"),
+         _is(v, dt, new, dev, "v"), H, qp if q_out is None else _is(q_out, dt, (T, H, D), dev, "q_out")),
+        "qlora_kv_append")
 
 
 def qlora_paged_attn_workspace_bytes(cache: KVCache, kv: KVBatch, heads: int) -> int:
-    with _On(cache.device, None):
+    with torch.cuda.device(cache._index):
         n = lib.qlora_paged_attn_workspace_bytes(cache._ref, kv._ref, heads)
     _need(n > 0, "not a valid cache, batch and head count")
     return n
@@ -608,14 +607,13 @@ def qlora_paged_attn_fwd(cache: KVCache, kv: KVBatch, q, out, scale: float, work
                          lse=None, stream=None):
     """q and out [tokens, heads, head_dim]; lse: float32 [tokens, heads] or None."""
     _need(q.dim() == 3, "q: need [tokens, heads, head_dim]")
-    _need(cache.device == kv.device and workspace.device == kv.device, "cache, batch and workspace on different devices")
+    T, H, dt, dev = kv.tokens, q.shape[1], cache.dtype, cache._index
+    _need(dev == kv._index and dev == workspace.get_device(), "cache, batch and workspace on different devices")
     _need(workspace.is_contiguous(), "workspace: need a contiguous tensor")
-    T, H, dt, dev = kv.tokens, q.shape[1], cache.dtype, cache.device
     shape = (T, H, cache.head_dim)
     qp, op = _is(q, dt, shape, dev, "q"), _is(out, dt, shape, dev, "out")
     _need(qp != op, "out may not be q")
-    args = (cache._ref, kv._ref, qp, H, scale, window, sinks, op,
-            None if lse is None else _is(lse, torch.float32, (T, H), dev, "lse"), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
-    with _On(dev, stream) as s:
-        _check(lib.qlora_paged_attn_fwd(*args, s), "qlora_paged_attn_fwd")
+    _on(dev, stream, lib.qlora_paged_attn_fwd,
+        (cache._ref, kv._ref, qp, H, scale, window, sinks, op,
+         None if lse is None else _is(lse, torch.float32, (T, H), dev, "lse"), workspace.data_ptr(), workspace.nbytes),
+        "qlora_paged_attn_fwd")

@@ -168,7 +168,7 @@ qlora_status launch_decode(AttnParams &p, const DeviceInfo &dev, cudaStream_t s)
         LaunchScope ls(QLORA_KERNEL_ATTENTION, s);
         QLORA_CUDA_TRY(launch_pdl(decode_kernel<DP, F16>, dim3(grid), dim3(C::kThreads), C::kBytes, s, p));
     }
-    if (!p.whole_items) {
+    {
         LaunchScope ls(QLORA_KERNEL_ATTENTION, s);
         QLORA_CUDA_TRY(launch_pdl(combine_kernel<C::kRows, DP, F16>, dim3(grid, C::kRows / 8), dim3(256), 0, s, p));
     }

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
     const uint32_t tmem = bars->tmem;
     W walk;
     if (warp == 8) {
-        walk.init(v, pre, cta < G ? cta * total / G : 0, cta < G ? (cta + 1) * total / G : 0, p.whole_items);
+        walk.init(v, pre, cta < G ? first_unit(cta, G, total) : 0, cta < G ? first_unit(cta + 1, G, total) : 0);
         fence_proxy_async_smem();
     }
     __syncthreads();   // the prefix sums have been read: the ring is free

@@ -57,7 +57,6 @@ struct AttnParams {
     float *part;
     Desc *desc;
     float scale_log2;     // softmax scale * log2 e
-    int whole_items;      // no item is cut: a CTA takes the items that begin in its units
     int *err;
     uint64_t timeout_ns;
 };
@@ -146,7 +145,7 @@ __device__ __forceinline__ void schedule_scan(const BatchView &v, int64_t *pre)
     int64_t *warp_sum = pre + NT + 1;
     const int tid = threadIdx.x, lane = tid & 31, run = (v.batch + NT - 1) / NT;
     int64_t mine = 0;
-    if (v.batch <= NT / 8) {   // few requests, maybe of many row tiles: a warp for each, its lanes take the tiles
+    if (ROWS > 16 && v.batch <= NT / 8) {   // few requests, maybe of many row tiles: a warp for each, its lanes take the tiles
         for (int b = tid >> 5; b < v.batch; b += NT / 32) {
             const Request r = load_request(v, b);
             const int n = row_tiles<ROWS>(v, r);
@@ -182,6 +181,18 @@ __device__ __forceinline__ void schedule_scan(const BatchView &v, int64_t *pre)
     __syncthreads();
 }
 
+// a / b of nonnegative numbers; 32-bit whenever they are (a 64-bit division takes some 250 cycles, and several of
+// them stand before a CTA's first copy).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
+// The CTA that takes unit e - 1, of G that share W units; a CTA's first unit.
+__device__ __forceinline__ int cta_of_last(int64_t e, int64_t G, int64_t W) { return (int)quotient(e * G - 1, W); }
+__device__ __forceinline__ int64_t first_unit(int64_t cta, int64_t G, int64_t W) { return quotient(cta * W, G); }
+
 // Walks a CTA's items.  Every lane of a warp runs it with the same values.
 template <int NT, int ROWS, int TILE, int OV>
 struct Walker {
@@ -189,13 +200,11 @@ struct Walker {
     int64_t start;        // first unit of the current item
     int b, h, rt, n_rt;
     Request r;
-    bool whole_items;
 
-    __device__ __forceinline__ void init(const BatchView &v, const int64_t *pre, int64_t from, int64_t to, bool whole)
+    __device__ __forceinline__ void init(const BatchView &v, const int64_t *pre, int64_t from, int64_t to)
     {
         u = from;
         u1 = to;
-        whole_items = whole;
         if (u >= u1) return;
         int lo = 0, hi = NT;   // the last run that begins at or before `from`
         while (hi - lo > 1) {
@@ -207,7 +216,7 @@ struct Walker {
         if (run == 1) {
             b = lo;
             start = pre[lo];
-            per_head = (pre[lo + 1] - start) / v.kv_heads;
+            per_head = quotient(pre[lo + 1] - start, v.kv_heads);
         } else {   // the request inside the run: 32 at a time, one per lane
             const int b_end = min((lo + 1) * run, v.batch);
             int64_t base = pre[lo];
@@ -233,7 +242,7 @@ struct Walker {
         }
         r = load_request(v, b);
         n_rt = row_tiles<ROWS>(v, r);
-        h = (int)((from - start) / per_head);
+        h = (int)quotient(from - start, per_head);
         start += h * per_head;
         for (rt = 0;; rt += 32) {   // the row tile: 32 at a time (past the last one: cost 0)
             int incl = rt + lane < n_rt ? max(item_tiles<ROWS, TILE>(v, r, rt + lane).n, 1) + OV : 0;
@@ -252,10 +261,6 @@ struct Walker {
             }
             start += __shfl_sync(0xffffffffu, incl, 31);
             if (rt + 32 >= n_rt) break;   // not reached: `from` lies inside the head
-        }
-        if (whole && start < from) {   // begins in the CTA before
-            const int64_t c = max(item_tiles<ROWS, TILE>(v, r, rt).n, 1) + OV;
-            step(v, c);
         }
     }
 
@@ -282,7 +287,7 @@ struct Walker {
         while (u < u1 && start < u1) {
             const Tiles tl = item_tiles<ROWS, TILE>(v, r, rt);
             const int64_t cost = max(tl.n, 1) + OV, end = start + cost;
-            const int64_t lo = whole_items ? start : max(u, start), hi = whole_items ? end : min(u1, end);
+            const int64_t lo = max(u, start), hi = min(u1, end);
             it.b = b;
             it.h = h;
             it.rt = rt;
@@ -300,9 +305,6 @@ struct Walker {
         return false;
     }
 };
-
-// The CTA that takes unit e - 1, of G that share W units.
-__device__ __forceinline__ int cta_of_last(int64_t e, int64_t G, int64_t W) { return (int)((e * G - 1) / W); }
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2, int c3)
 {

@@ -23,7 +23,7 @@ namespace attn {
 template <int DP>
 struct DecodeCfg {
     static constexpr int kWarps = 4, kThreads = 32 * kWarps;
-    static constexpr int kRows = 16, kTile = 16 * kWarps, kOv = 0;
+    static constexpr int kRows = 16, kTile = 16 * kWarps, kOv = 3;
     static constexpr int kStages = DP == 128 ? 2 : 4;
     static constexpr uint32_t kStageBytes = 2 * 16 * DP * 2;   // keys, then values, of 16 positions
     static constexpr uint32_t kRing = kWarps * kStages * kStageBytes;
@@ -100,11 +100,12 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
     const int64_t G = min((int64_t)gridDim.x, total), cta = blockIdx.x;
     if (threadIdx.x == 0) p.desc[cta].parts = 0;
     if (cta >= G) return;
-    const int64_t from = cta * total / G, to = (cta + 1) * total / G;
+    const int64_t from = first_unit(cta, G, total), to = first_unit(cta + 1, G, total);
 
     // ---- producer: one 16-position step of the next item that has any ----
-    W wp;
-    wp.init(v, pre, from, to, p.whole_items);
+    W wp, wc;   // the producer's walk, and the consumer's
+    wp.init(v, pre, from, to);
+    wc = wp;
     Item pi;
     bool p_more = wp.next(v, pi);
     int pt = p_more ? pi.t0 : 0, p_item = 0, produced = 0, cache_t = -64, cache_page = -1;
@@ -120,6 +121,13 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                 pt = pi.t0;
                 p_item++;
                 cache_t = -64;
+                if (p_more && warp == 0) {   // its query rows, for the consumer: two lanes a row, a line each
+                    const int g = pi.rt * C::kRows + (lane >> 1), tok = v.token_of(g);
+                    if (g < pi.r.qn * v.group && (lane & 1) * 64 < v.head_dim)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                            static_cast<const uint16_t *>(p.q) +
+                            ((int64_t)(pi.r.q0 + tok) * v.heads + pi.h * v.group + g - tok * v.group) * v.head_dim + (lane & 1) * 64));
+                }
                 continue;
             }
             const int t = pt++;
@@ -151,8 +159,6 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
     for (int s = 0; s < ST; s++) produce();
 
     // ---- consumer ----
-    W wc;
-    wc.init(v, pre, from, to, p.whole_items);
     Item it;
     int consumed = 0;
     for (int item = 0; wc.next(v, it); item++) {
@@ -170,7 +176,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
             [[maybe_unused]] const int64_t q_n = (int64_t)v.tokens * v.heads * v.head_dim;
             auto row_ptr = [&](int r) -> const uint32_t * {
                 const int g = gr0 + r;
-                const int64_t o = ((int64_t)(it.r.q0 + g / v.group) * v.heads + it.h * v.group + g % v.group) * v.head_dim;
+                const int64_t o = ((int64_t)(it.r.q0 + v.token_of(g)) * v.heads + it.h * v.group + g - v.token_of(g) * v.group) * v.head_dim;
                 return QLORA_IN(o + v.head_dim - 1, q_n)
                            ? reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.q) + o)
                            : nullptr;
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
             if (it.whole) {
                 const float inv = L > 0.0f ? 1.0f / L : 0.0f;
                 const int g = gr0 + r;
-                const int64_t row = (int64_t)(it.r.q0 + g / v.group) * v.heads + it.h * v.group + g % v.group;
+                const int64_t row = (int64_t)(it.r.q0 + v.token_of(g)) * v.heads + it.h * v.group + g - v.token_of(g) * v.group;
                 const int64_t at = row * v.head_dim + c;
                 if (c < v.head_dim && QLORA_IN(at + 3, out_n))
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =

@@ -25,10 +25,10 @@ namespace {
 // the count may be updated in place: it is read before the cluster's barrier
 // and written after it.
 //
-// The call moves a few hundred KB at most; what bounds it is latency (one
-// launch, two dependent reads, three scans).
-
-constexpr int kPlanThreads = 512;
+// The call moves a few hundred KB at most; what bounds it is latency (a launch,
+// three dependent reads, two scans), so a small batch gets one small CTA and a large
+// one as many threads as a cluster has; a thread takes four neighbouring
+// tokens, which mostly share the search.
 
 struct PlanParams {
     const int32_t *ctx, *qlen;
@@ -39,27 +39,37 @@ struct PlanParams {
     int batch, max_pages, tokens, num_pages, page_shift;
 };
 
-// Exclusive prefix of one value per thread over the block, and the total.
-__device__ __forceinline__ int64_t block_scan(int64_t mine, int64_t *warp_sum, int64_t &total)
+// Exclusive prefixes of two values per thread over the block, and their totals.
+struct Two {
+    int64_t a, b;
+};
+__device__ __forceinline__ Two block_scan(Two mine, Two *warp_sum, Two &total)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl = mine;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    Two incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+        const int64_t ua = __shfl_up_sync(0xffffffffu, incl.a, o), ub = __shfl_up_sync(0xffffffffu, incl.b, o);
+        if (lane >= o) {
+            incl.a += ua;
+            incl.b += ub;
+        }
     }
-    __syncthreads();
+    __syncthreads();   // the sums of the scan before have been read
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < kPlanThreads / 32; w++) {
-        const int64_t s = warp_sum[w];
-        if (w < warp) before += s;
-        total += s;
+    Two before{0, 0};
+    total = Two{0, 0};
+    for (int w = 0; w < warps; w++) {
+        const Two s = warp_sum[w];
+        if (w < warp) {
+            before.a += s.a;
+            before.b += s.b;
+        }
+        total.a += s.a;
+        total.b += s.b;
     }
-    return before + incl - mine;
+    return Two{before.a + incl.a - mine.a, before.b + incl.b - mine.b};
 }
 
 // The index i with pre[i] <= x < pre[i + 1] (pre ascending, pre[0] <= x < pre[n]).
@@ -75,16 +85,17 @@ __device__ __forceinline__ int owner_of(const int32_t *pre, int n, int x)
 
 __device__ __forceinline__ int32_t clamp31(int64_t x) { return (int32_t)min(x, (int64_t)INT32_MAX); }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
+__global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
 {
     extern __shared__ int32_t plan_smem[];
-    __shared__ int64_t warp_sum[kPlanThreads / 32];
-    const int n = p.batch, tid = threadIdx.x;
+    __shared__ Two warp_sum[32];
+    const int n = p.batch, tid = threadIdx.x, threads = blockDim.x;
     int32_t *rows_pre = plan_smem;             // [n + 1] rows before request i, at most `tokens`
     int32_t *back_pre = rows_pre + n + 1;      // pages returned before i
     int32_t *take_pre = back_pre + n + 1;      // pages asked for before i
+    int32_t *ctx_of = take_pre + n + 1;        // [n] ctx_len, -1 for a request that is refused or has ended
     const int rank = (int)sm100::cluster_ctarank(), ctas = (int)sm100::cluster_nctarank();
-    const int64_t step = (int64_t)ctas * kPlanThreads, first = (int64_t)rank * kPlanThreads + tid;
+    const int64_t step = (int64_t)ctas * threads, first = (int64_t)rank * threads + tid;
     sm100::pdl_wait();
     sm100::pdl_trigger();
     const int page = 1 << p.page_shift;
@@ -92,35 +103,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     auto pages = [&](int64_t t) { return (t + page - 1) >> p.page_shift; };
     const int64_t capacity = (int64_t)p.max_pages << p.page_shift;
 
-    int64_t rows_at = 0, back_at = 0, take_at = 0;
-    for (int b0 = 0; b0 < n; b0 += kPlanThreads) {
+    Two at{0, 0};            // rows and returned pages so far
+    int64_t take_at = 0;
+    for (int b0 = 0; b0 < n; b0 += threads) {
         const int b = b0 + tid;
         const int64_t ctx = b < n ? p.ctx[b] : 0, q = b < n ? p.qlen[b] : 0;
         const int64_t rows = max(q, (int64_t)0);
         const int64_t back = q < 0 ? min(pages(max(ctx, (int64_t)0)), (int64_t)p.max_pages) : 0;
-        int64_t total;
-        const int64_t rows0 = rows_at + block_scan(rows, warp_sum, total);
-        rows_at += total;
-        const int64_t back0 = back_at + block_scan(back, warp_sum, total);
-        back_at += total;
-        const bool fits = q >= 0 && ctx >= 0 && ctx + rows <= capacity && rows0 + rows <= p.tokens;
+        Two total;
+        const Two pre = block_scan(Two{rows, back}, warp_sum, total);
+        const int64_t rows0 = at.a + pre.a, back0 = at.b + pre.b;
+        at.a += total.a;
+        at.b += total.b;
+        const bool fits = q >= 0 && ctx >= 0 && ctx + rows <= capacity && (rows == 0 || rows0 + rows <= p.tokens);
         const int64_t take = fits ? pages(ctx + rows) - pages(ctx) : 0;
-        const int64_t take0 = take_at + block_scan(take, warp_sum, total);
-        take_at += total;
+        const int64_t take0 = take_at + block_scan(Two{take, 0}, warp_sum, total).a;
+        take_at += total.a;
         if (b < n) {
             rows_pre[b] = (int32_t)min(rows0, (int64_t)p.tokens);
             back_pre[b] = clamp31(back0);
             take_pre[b] = clamp31(take0);
+            ctx_of[b] = fits ? (int32_t)ctx : -1;
         }
     }
     if (tid == 0) {
-        rows_pre[n] = (int32_t)min(rows_at, (int64_t)p.tokens);
-        back_pre[n] = clamp31(back_at);
+        rows_pre[n] = (int32_t)min(at.a, (int64_t)p.tokens);
+        back_pre[n] = clamp31(at.b);
         take_pre[n] = clamp31(take_at);
     }
     __syncthreads();
     // a valid call returns no more pages than are not in the pool
-    const int pool = (int)min((int64_t)count + back_at, (int64_t)p.num_pages);
+    const int pool = (int)min((int64_t)count + at.b, (int64_t)p.num_pages);
     const int returned = pool - count;
     // requests take pages in order, and none after the first that the pool cannot serve
     int lo = 0, hi = n + 1;
@@ -132,44 +145,51 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p)
     auto pool_page = [&](int j) -> int32_t {
         if (j < count) return p.free_pages[j];
         const int r = j - count, b = owner_of(back_pre, n, r);
-        const int64_t at = (int64_t)b * p.max_pages + r - back_pre[b];
-        return QLORA_IN(at, (int64_t)n * p.max_pages) ? p.table[at] : -1;
+        const int64_t i = (int64_t)b * p.max_pages + r - back_pre[b];
+        return QLORA_IN(i, (int64_t)n * p.max_pages) ? p.table[i] : -1;
     };
-    auto granted = [&](int b, int64_t ctx, int64_t q) {
-        const int64_t rows = max(q, (int64_t)0);
-        if (q < 0 || ctx < 0 || ctx + rows > capacity || rows_pre[b] + rows > p.tokens) return false;
-        return pages(ctx + rows) == pages(ctx) || take_pre[b + 1] <= pool;
-    };
+    // Whether request b, which fits, gets its pages.  (The prefix counts what refused requests
+    // asked for too; that is at most tokens / 16 + batch pages, so it stays in 32 bits.)
+    auto granted = [&](int b) { return take_pre[b + 1] == take_pre[b] || take_pre[b + 1] <= pool; };
 
     for (int64_t b = first; b <= n; b += step) {
         p.cu_q[b] = rows_pre[b];
         if (b == n) break;
-        const int64_t ctx = p.ctx[b], q = p.qlen[b];
-        p.kv_len[b] = granted((int)b, ctx, q) ? (int32_t)(ctx + q) : 0;
+        const bool ok = ctx_of[b] >= 0 && granted((int)b);
+        p.kv_len[b] = ok ? ctx_of[b] + max(p.qlen[b], 0) : 0;
     }
     for (int64_t r = first; r < returned; r += step)
         if (QLORA_IN(count + r, p.num_pages)) p.free_pages[count + r] = pool_page((int)(count + r));
     for (int64_t u = first; u < used; u += step) {
         const int b = owner_of(take_pre, n, (int)u);
-        const int64_t at = (int64_t)b * p.max_pages + pages(p.ctx[b]) + u - take_pre[b];
-        if (QLORA_IN(at, (int64_t)n * p.max_pages)) p.table[at] = pool_page(pool - 1 - (int)u);
+        const int64_t i = (int64_t)b * p.max_pages + pages(ctx_of[b]) + u - take_pre[b];
+        if (QLORA_IN(i, (int64_t)n * p.max_pages)) p.table[i] = pool_page(pool - 1 - (int)u);
     }
     const int all_rows = rows_pre[n];
-    for (int64_t t = first; t < p.tokens; t += step) {
-        int32_t pos = -1, slot = -1;
-        if (t < all_rows) {
-            const int b = owner_of(rows_pre, n, (int)t);
-            const int64_t ctx = p.ctx[b];
-            if (granted(b, ctx, p.qlen[b])) {
-                pos = (int32_t)(ctx + t - rows_pre[b]);
-                const int held = (int)pages(ctx), i = pos >> p.page_shift;
-                const int32_t id = i < held ? p.table[(int64_t)b * p.max_pages + i]
-                                            : pool_page(pool - 1 - (take_pre[b] + i - held));
-                if ((unsigned)id < (unsigned)p.num_pages) slot = (id << p.page_shift) + (pos & (page - 1));
+    for (int64_t t4 = 4 * first; t4 < p.tokens; t4 += 4 * step) {
+        int32_t pos[4], slot[4];
+        int b = t4 < all_rows ? owner_of(rows_pre, n, (int)t4) : n;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int t = (int)t4 + k;
+            pos[k] = slot[k] = -1;
+            if (t >= all_rows) continue;
+            while (rows_pre[b + 1] <= t) b++;
+            if (ctx_of[b] < 0 || !granted(b)) continue;
+            pos[k] = ctx_of[b] + t - rows_pre[b];
+            const int held = (int)pages(ctx_of[b]), i = pos[k] >> p.page_shift;
+            const int32_t id = i < held ? p.table[(int64_t)b * p.max_pages + i] : pool_page(pool - 1 - (take_pre[b] + i - held));
+            if ((unsigned)id < (unsigned)p.num_pages) slot[k] = (id << p.page_shift) + (pos[k] & (page - 1));
+        }
+        if (t4 + 4 <= p.tokens) {
+            *reinterpret_cast<int4 *>(p.positions + t4) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4 *>(p.slots + t4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+            for (int k = 0; k < (int)(p.tokens - t4); k++) {
+                p.positions[t4 + k] = pos[k];
+                p.slots[t4 + k] = slot[k];
             }
         }
-        p.positions[t] = pos;
-        p.slots[t] = slot;
     }
     // every CTA has read the count
     if (ctas > 1) sm100::cluster_sync(); else __syncthreads();
@@ -243,10 +263,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         }
     }
     __syncthreads();
-    const int per_token = (p.heads + 2 * p.kv_heads) * groups;
+    // thread: piece i0 of every stride-th head, counted over the block's tokens
+    const int per_token = p.heads + 2 * p.kv_heads, lanes = kAppendThreads / groups;
+    const int i0 = ((int)threadIdx.x % groups) * 8, stride = lanes * (int)gridDim.y;
+    if ((int)threadIdx.x >= lanes * groups) return;
     const int64_t slots = (int64_t)p.num_pages << p.page_shift;
-    for (int e = blockIdx.y * kAppendThreads + threadIdx.x; e < toks * per_token; e += gridDim.y * kAppendThreads) {
-        const int tk = e / per_token, u = e % per_token, head = u / groups, i0 = (u % groups) * 8;
+    int head = blockIdx.y * lanes + (int)threadIdx.x / groups, tk = 0;
+    for (;; head += stride) {
+        while (head >= per_token) {
+            head -= per_token;
+            tk++;
+        }
+        if (tk >= toks) break;
         const int64_t slot = slot_of[tk], t = t0 + tk;
         if (slot < 0 || slot >= slots) continue;   // padding, a refused request, or not a place of the cache
         const uint16_t *src;
@@ -369,17 +397,18 @@ extern "C" qlora_status qlora_kv_plan(const qlora_kv_batch *kv, int32_t page_siz
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     PlanParams p{ctx_len, q_len, free_pages, free_count, free_count_out, kv->block_table, kv->cu_q, kv->kv_len,
                  kv->positions, kv->slots, kv->batch, kv->max_pages, kv->tokens, num_pages, page_shift(page_size)};
-    const size_t smem = 3 * ((size_t)kv->batch + 1) * 4;   // at most 49,164 bytes
+    const size_t smem = 4 * ((size_t)kv->batch + 1) * 4;   // at most 65,552 bytes
     static PerDeviceOnce once;
     QLORA_TRY(once.run(dev.device, [] {
         QLORA_CUDA_TRY(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            3 * (kMaxRequests + 1) * 4));
+                                            4 * (kMaxRequests + 1) * 4));
         return QLORA_OK;
     }));
     cudaLaunchConfig_t cfg{};
-    const int ctas = kv->tokens <= 2 * kPlanThreads ? 1 : 8;
+    const bool small = kv->tokens <= 512 && kv->batch <= 128;
+    const int ctas = small ? 1 : 8;
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kPlanThreads);
+    cfg.blockDim = dim3(small ? 128 : 1024);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -433,11 +462,11 @@ extern "C" qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora
     if (rope)
         for (int i = 0; i < 64; i++) p.turns[i] = rope->turns[i];
     // as many tokens per block as leave two blocks for every SM; with few tokens, several blocks per token
-    const int pieces = (heads + 2 * cache->kv_heads) * (cache->head_dim / 16);
+    const int per_block = kAppendThreads / (cache->head_dim / 16);   // heads at once
     p.block_tokens = std::max(1, std::min(kAppendTokens, kv->tokens / (2 * dev.sms)));
     const int blocks = (kv->tokens + p.block_tokens - 1) / p.block_tokens;
     int split = std::max(1, 2 * dev.sms / blocks);
-    split = std::min(split, (p.block_tokens * pieces + kAppendThreads - 1) / kAppendThreads);
+    split = std::min(split, (p.block_tokens * (heads + 2 * cache->kv_heads) + per_block - 1) / per_block);
     {
         LaunchScope ls(QLORA_KERNEL_BLOCK, s);
         const dim3 grid((unsigned)blocks, (unsigned)split);
