@@ -58,18 +58,23 @@ __device__ __forceinline__ Two block_scan(Two mine, Two *warp_sum, Two &total)
     __syncthreads();   // the sums of the scan before have been read
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    Two before{0, 0};
-    total = Two{0, 0};
-    for (int w = 0; w < warps; w++) {
-        const Two s = warp_sum[w];
-        if (w < warp) {
-            before.a += s.a;
-            before.b += s.b;
+    if (warp == 0) {   // (every warp adding up the sums on its own took three times as long with 32 of them)
+        Two s = lane < warps ? warp_sum[lane] : Two{0, 0};
+        const Two own = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t ua = __shfl_up_sync(0xffffffffu, s.a, o), ub = __shfl_up_sync(0xffffffffu, s.b, o);
+            if (lane >= o) {
+                s.a += ua;
+                s.b += ub;
+            }
         }
-        total.a += s.a;
-        total.b += s.b;
+        if (lane == 31) warp_sum[32] = s;
+        warp_sum[lane] = Two{s.a - own.a, s.b - own.b};
     }
-    return Two{before.a + incl.a - mine.a, before.b + incl.b - mine.b};
+    __syncthreads();
+    total = warp_sum[32];
+    return Two{warp_sum[warp].a + incl.a - mine.a, warp_sum[warp].b + incl.b - mine.b};
 }
 
 // The index i with pre[i] <= x < pre[i + 1] (pre ascending, pre[0] <= x < pre[n]).
@@ -88,7 +93,7 @@ __device__ __forceinline__ int32_t clamp31(int64_t x) { return (int32_t)min(x, (
 __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
 {
     extern __shared__ int32_t plan_smem[];
-    __shared__ Two warp_sum[32];
+    __shared__ Two warp_sum[33];
     const int n = p.batch, tid = threadIdx.x, threads = blockDim.x;
     int32_t *rows_pre = plan_smem;             // [n + 1] rows before request i, at most `tokens`
     int32_t *back_pre = rows_pre + n + 1;      // pages returned before i
@@ -142,11 +147,12 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
         if (take_pre[mid] <= pool) lo = mid; else hi = mid;
     }
     const int used = take_pre[lo];
-    auto pool_page = [&](int j) -> int32_t {
-        if (j < count) return p.free_pages[j];
+    // where the id of page j of the pool stands
+    auto pool_page = [&](int j) -> const int32_t * {
+        if (j < count) return p.free_pages + j;
         const int r = j - count, b = owner_of(back_pre, n, r);
         const int64_t i = (int64_t)b * p.max_pages + r - back_pre[b];
-        return QLORA_IN(i, (int64_t)n * p.max_pages) ? p.table[i] : -1;
+        return QLORA_IN(i, (int64_t)n * p.max_pages) ? p.table + i : p.table;
     };
     // Whether request b, which fits, gets its pages.  (The prefix counts what refused requests
     // asked for too; that is at most tokens / 16 + batch pages, so it stays in 32 bits.)
@@ -159,28 +165,34 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
         p.kv_len[b] = ok ? ctx_of[b] + max(p.qlen[b], 0) : 0;
     }
     for (int64_t r = first; r < returned; r += step)
-        if (QLORA_IN(count + r, p.num_pages)) p.free_pages[count + r] = pool_page((int)(count + r));
-    for (int64_t u = first; u < used; u += step) {
+        if (QLORA_IN(count + r, p.num_pages)) p.free_pages[count + r] = *pool_page((int)(count + r));
+    for (int64_t u = step - 1 - first; u < used; u += step) {   // (the last threads have the least to do below)
         const int b = owner_of(take_pre, n, (int)u);
         const int64_t i = (int64_t)b * p.max_pages + pages(ctx_of[b]) + u - take_pre[b];
-        if (QLORA_IN(i, (int64_t)n * p.max_pages)) p.table[i] = pool_page(pool - 1 - (int)u);
+        if (QLORA_IN(i, (int64_t)n * p.max_pages)) p.table[i] = *pool_page(pool - 1 - (int)u);
     }
     const int all_rows = rows_pre[n];
     for (int64_t t4 = 4 * first; t4 < p.tokens; t4 += 4 * step) {
         int32_t pos[4], slot[4];
+        const int32_t *id_at[4];   // four loads that do not wait for one another
         int b = t4 < all_rows ? owner_of(rows_pre, n, (int)t4) : n;
 #pragma unroll
         for (int k = 0; k < 4; k++) {
             const int t = (int)t4 + k;
-            pos[k] = slot[k] = -1;
+            pos[k] = -1;
+            id_at[k] = nullptr;
             if (t >= all_rows) continue;
             while (rows_pre[b + 1] <= t) b++;
             if (ctx_of[b] < 0 || !granted(b)) continue;
             pos[k] = ctx_of[b] + t - rows_pre[b];
             const int held = (int)pages(ctx_of[b]), i = pos[k] >> p.page_shift;
-            const int32_t id = i < held ? p.table[(int64_t)b * p.max_pages + i] : pool_page(pool - 1 - (take_pre[b] + i - held));
-            if ((unsigned)id < (unsigned)p.num_pages) slot[k] = (id << p.page_shift) + (pos[k] & (page - 1));
+            id_at[k] = i < held ? p.table + (int64_t)b * p.max_pages + i : pool_page(pool - 1 - (take_pre[b] + i - held));
         }
+#pragma unroll
+        for (int k = 0; k < 4; k++) slot[k] = id_at[k] ? *id_at[k] : -1;
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            slot[k] = (unsigned)slot[k] < (unsigned)p.num_pages ? (slot[k] << p.page_shift) + (pos[k] & (page - 1)) : -1;
         if (t4 + 4 <= p.tokens) {
             *reinterpret_cast<int4 *>(p.positions + t4) = make_int4(pos[0], pos[1], pos[2], pos[3]);
             *reinterpret_cast<int4 *>(p.slots + t4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
@@ -259,7 +271,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             const float rest = (float)(turn - rint(turn));
             float s, c;
             __sincosf(rest * 6.28318530718f, &s, &c);
-            cs[e] = make_float2(c, s);
+            // pair 8 g + j at j * groups + g: the threads of a warp, one piece g each, read neighbours
+            const int i = e % half;
+            cs[e - i + (i & 7) * groups + (i >> 3)] = make_float2(c, s);
         }
     }
     __syncthreads();
@@ -294,12 +308,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         }
         uint4 a = *reinterpret_cast<const uint4 *>(src + i0), b = *reinterpret_cast<const uint4 *>(src + i0 + half);
         if (rotate) {
-            const float2 *tab = cs + tk * half + i0;
+            const float2 *tab = cs + tk * half + (i0 >> 3);
             uint32_t *pa = reinterpret_cast<uint32_t *>(&a), *pb = reinterpret_cast<uint32_t *>(&b);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const float2 x = up2<F16>(pa[j]), y = up2<F16>(pb[j]);
-                const float2 c0 = tab[2 * j], c1 = tab[2 * j + 1];
+                const float2 c0 = tab[2 * j * groups], c1 = tab[(2 * j + 1) * groups];
                 pa[j] = down2<F16>(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
                 pb[j] = down2<F16>(x.x * c0.y + y.x * c0.x, x.y * c1.y + y.y * c1.x);
             }
