@@ -47,6 +47,7 @@ EXPORTS = (
     "qlora_dequantize_nf4_dq_ex",
     "qlora_kv_plan", "qlora_build_rope", "qlora_kv_append",
     "qlora_paged_attn_workspace_bytes", "qlora_paged_attn_fwd",
+    "qlora_block_cached_workspace_bytes", "qlora_block_fwd_cached",
 )
 
 KERNEL_KINDS = ("quantize", "dq_encode", "dequantize", "fwd_fused", "bwd_fused", "lowrank", "wgrad",
@@ -152,6 +153,8 @@ def _load():
         "qlora_kv_append": (ctypes.c_int, [P, P, P, P, P, P, I32, P, P]),
         "qlora_paged_attn_workspace_bytes": (S, [P, P, I32]),
         "qlora_paged_attn_fwd": (ctypes.c_int, [P, P, P, I32, F, I32, I32, P, P, P, S, P]),
+        "qlora_block_cached_workspace_bytes": (S, [P, P, P]),
+        "qlora_block_fwd_cached": (ctypes.c_int, [P, P, P, P, P, P, I32, I32, P, S, P]),
         "qlora_block_bwd": (ctypes.c_int, [ctypes.POINTER(qlora_block), P, P, P, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
@@ -617,3 +620,24 @@ def qlora_paged_attn_fwd(cache: KVCache, kv: KVBatch, q, out, scale: float, work
         (cache._ref, kv._ref, qp, H, scale, window, sinks, op,
          None if lse is None else _is(lse, torch.float32, (T, H), dev, "lse"), workspace.data_ptr(), workspace.nbytes),
         "qlora_paged_attn_fwd")
+
+
+def qlora_block_cached_workspace_bytes(block: Block, cache: KVCache, kv: KVBatch) -> int:
+    with torch.cuda.device(cache._index):
+        n = lib.qlora_block_cached_workspace_bytes(ctypes.addressof(block.desc), cache._ref, kv._ref)
+    _need(n > 0, "block, cache and batch do not go together")
+    return n
+
+
+def qlora_block_fwd_cached(block: Block, cache: KVCache, kv: KVBatch, rope, x, y, workspace, window: int = 0,
+                           sinks: int = 0, stream=None):
+    """x and y bf16 [tokens, hidden]; block.batch and block.seq are not used."""
+    dev, shape = cache._index, (kv.tokens, block.desc.hidden)
+    _need(dev == kv._index and dev == workspace.get_device() and dev == block.norm1.get_device(),
+          "block, cache, batch and workspace on different devices")
+    _need(workspace.is_contiguous(), "workspace: need a contiguous tensor")
+    xp, yp = _is(x, torch.bfloat16, shape, dev, "x"), _is(y, torch.bfloat16, shape, dev, "y")
+    _need(xp != yp, "y may not be x")
+    _on(dev, stream, lib.qlora_block_fwd_cached,
+        (ctypes.addressof(block.desc), cache._ref, kv._ref, ctypes.addressof(rope), xp, yp, window, sinks,
+         workspace.data_ptr(), workspace.nbytes), "qlora_block_fwd_cached")

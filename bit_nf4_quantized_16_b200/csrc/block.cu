@@ -23,6 +23,7 @@
 
 #include "block_kernels.cuh"
 #include "common.cuh"
+#include "serve.cuh"
 
 namespace qlora {
 namespace {
@@ -97,12 +98,11 @@ BlockLayout layout(const qlora_block *b)
     return L;
 }
 
-qlora_status check_block(const qlora_block *b)
+// The parts of a description that both forms of the block use.
+qlora_status check_parts(const qlora_block *b)
 {
-    if (!b) return QLORA_ERR_INVALID_ARG;
-    if (b->batch < 1 || b->seq < 1 || b->heads < 1 || b->head_dim < 8 || b->hidden < 8 || b->inter < 8)
-        return QLORA_ERR_SHAPE;
-    if (b->head_dim % 16 || b->hidden % 64 || b->inter % 64 || b->seq % 8) return QLORA_ERR_SHAPE;
+    if (b->heads < 1 || b->head_dim < 8 || b->hidden < 8 || b->inter < 8) return QLORA_ERR_SHAPE;
+    if (b->head_dim % 16 || b->hidden % 64 || b->inter % 64) return QLORA_ERR_SHAPE;
     if ((int64_t)b->heads * b->head_dim != b->hidden) return QLORA_ERR_SHAPE;
     const int64_t want[kL][2] = {{b->hidden, b->hidden}, {b->hidden, b->hidden}, {b->hidden, b->hidden},
                                  {b->hidden, b->hidden}, {b->inter, b->hidden}, {b->inter, b->hidden},
@@ -113,8 +113,16 @@ qlora_status check_block(const qlora_block *b)
     }
     if (!b->norm1 || !b->norm2) return QLORA_ERR_INVALID_ARG;
     if (!aligned16(b->norm1) || !aligned16(b->norm2)) return QLORA_ERR_ALIGNMENT;
-    if (!(b->rms_eps >= 0.0f) || !(b->rope_base > 1.0f)) return QLORA_ERR_INVALID_ARG;
+    if (!(b->rms_eps >= 0.0f)) return QLORA_ERR_INVALID_ARG;
     return QLORA_OK;
+}
+
+qlora_status check_block(const qlora_block *b)
+{
+    if (!b) return QLORA_ERR_INVALID_ARG;
+    if (b->batch < 1 || b->seq < 1 || b->seq % 8) return QLORA_ERR_SHAPE;
+    QLORA_TRY(check_parts(b));
+    return b->rope_base > 1.0f ? QLORA_OK : QLORA_ERR_INVALID_ARG;
 }
 
 using bf16 = __nv_bfloat16;
@@ -279,10 +287,123 @@ qlora_status forward(const Ctx &c, const bf16 *x, bf16 *y, bool save)
     return launch_status();
 }
 
+// ---- the serving form --------------------------------------------------------------
+// The same layer over the new tokens of many requests: its attention reads a
+// paged cache that the step's keys and values have been appended to.
+
+qlora_status check_cached(const qlora_block *b, const qlora_kv_cache *c, const qlora_kv_batch *kv)
+{
+    if (!b || !c || !kv) return QLORA_ERR_INVALID_ARG;
+    QLORA_TRY(check_parts(b));
+    if (c->kv_heads != b->heads || c->head_dim != b->head_dim) return QLORA_ERR_SHAPE;
+    if (b->r < 8 || b->r > 128 || b->r % 8) return QLORA_ERR_SHAPE;   // as the linears ask, before anything is launched
+    if (c->dtype != QLORA_BF16) return QLORA_ERR_INVALID_ARG;
+    return QLORA_OK;
+}
+
+// Only the buffers that the serving form uses are laid out; `sc` is the attention's workspace.
+BlockLayout layout_cached(const qlora_block *b, int64_t tokens, size_t attn_bytes)
+{
+    BlockLayout L{};
+    L.T = tokens;
+    L.d = b->hidden;
+    L.I = b->inter;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off += al(bytes);
+        return o;
+    };
+    const size_t td = (size_t)L.T * L.d * 2, ti = (size_t)L.T * L.I * 2;
+    for (size_t *p : {&L.u1, &L.q, &L.k, &L.v, &L.a, &L.ao, &L.h, &L.u2}) *p = take(td);
+    for (size_t *p : {&L.gt, &L.up, &L.m}) *p = take(ti);
+    L.sc = take(attn_bytes);
+    size_t lin = 0;
+    for (int l = 0; l < kL; l++) {
+        const size_t n = qlora_linear_workspace_bytes(L.T, out_features(b, l), in_features(b, l), b->r);
+        lin = n > lin ? n : lin;
+    }
+    L.lin_bytes = lin;
+    L.lin = take(lin);
+    L.bytes = off;
+    return L;
+}
+
+qlora_status forward_cached(const Ctx &c, const qlora_kv_cache *cache, const qlora_kv_batch *kv,
+                            const qlora_rope *rope, const bf16 *x, bf16 *y, int32_t window, int32_t sinks,
+                            size_t attn_bytes)
+{
+    const qlora_block *b = c.b;
+    const BlockLayout &L = c.L;
+    auto norm = [&](const bf16 *in, const bf16 *res, bf16 *sum, const void *g, bf16 *out) {
+        LaunchScope ls(QLORA_KERNEL_BLOCK, c.s);
+        return launch_pdl(blk::rmsnorm_fwd_kernel, dim3((unsigned)L.T), dim3(256), 0, c.s, in, res, sum, (const bf16 *)g,
+                          (int)L.d, b->rms_eps, out, (float *)nullptr);
+    };
+    QLORA_CUDA_TRY(norm(x, nullptr, nullptr, b->norm1, c.at(L.u1)));
+    QLORA_TRY(lin_fwd(c, Lq, c.at(L.u1), c.at(L.q), nullptr));
+    QLORA_TRY(lin_fwd(c, Lk, c.at(L.u1), c.at(L.k), nullptr));
+    QLORA_TRY(lin_fwd(c, Lv, c.at(L.u1), c.at(L.v), nullptr));
+    QLORA_TRY(qlora_kv_append(cache, kv, rope, c.at(L.q), c.at(L.k), c.at(L.v), b->heads, c.at(L.q), c.s));
+    QLORA_TRY(qlora_paged_attn_fwd(cache, kv, c.at(L.q), b->heads, 1.0f / sqrtf((float)b->head_dim), window, sinks,
+                                   c.at(L.a), nullptr, c.at<char>(L.sc), attn_bytes, c.s));
+    QLORA_TRY(lin_fwd(c, Lo, c.at(L.a), c.at(L.ao), nullptr));
+    QLORA_CUDA_TRY(norm(x, c.at(L.ao), c.at(L.h), b->norm2, c.at(L.u2)));
+    QLORA_TRY(lin_fwd(c, Lgate, c.at(L.u2), c.at(L.gt), nullptr));
+    QLORA_TRY(lin_fwd(c, Lup, c.at(L.u2), c.at(L.up), nullptr));
+    {
+        LaunchScope ls(QLORA_KERNEL_BLOCK, c.s);
+        QLORA_CUDA_TRY(launch_pdl(blk::swiglu_fwd_kernel, dim3(grid_for(L.T * L.I / 8, c.sms)), dim3(256), 0, c.s,
+                                  (const bf16 *)c.at(L.gt), (const bf16 *)c.at(L.up), c.at(L.m), L.T * L.I));
+    }
+    // as in forward(): the residual add rides on a norm whose result is not used
+    QLORA_TRY(lin_fwd(c, Ldown, c.at(L.m), c.at(L.ao), nullptr));
+    QLORA_CUDA_TRY(norm(c.at(L.h), c.at(L.ao), y, b->norm2, c.at(L.u1)));
+    return launch_status();
+}
+
 }  // namespace
 }  // namespace qlora
 
 using namespace qlora;
+
+extern "C" size_t qlora_block_cached_workspace_bytes(const qlora_block *b, const qlora_kv_cache *cache,
+                                                     const qlora_kv_batch *kv)
+{
+    if (check_cached(b, cache, kv) != QLORA_OK) return 0;
+    const size_t attn = qlora_paged_attn_workspace_bytes(cache, kv, b->heads);
+    return attn ? layout_cached(b, kv->tokens, attn).bytes : 0;
+}
+
+extern "C" qlora_status qlora_block_fwd_cached(const qlora_block *b, const qlora_kv_cache *cache,
+                                               const qlora_kv_batch *kv, const qlora_rope *rope, const void *x, void *y,
+                                               int32_t window, int32_t sinks, void *workspace, size_t workspace_bytes,
+                                               void *stream)
+{
+    QLORA_TRY(check_cached(b, cache, kv));
+    if (!rope || !x || !y || !workspace || !kv->positions || !kv->slots || !kv->block_table || !kv->cu_q || !kv->kv_len)
+        return QLORA_ERR_INVALID_ARG;
+    if (window < 0 || sinks < 0) return QLORA_ERR_INVALID_ARG;
+    if (rope->head_dim != b->head_dim) return QLORA_ERR_SHAPE;
+    const void *all[] = {x, y, workspace, kv->positions, kv->slots, kv->block_table, kv->cu_q, kv->kv_len};
+    for (const void *a : all)
+        if (!aligned16(a)) return QLORA_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    QLORA_TRY(device_info(&dev));
+    // what is wrong with the cache or the batch shows here, before anything is launched
+    QLORA_TRY(check_cache(cache));
+    QLORA_TRY(check_batch(kv));
+    const size_t attn = qlora_paged_attn_workspace_bytes(cache, kv, b->heads);
+    if (!attn) return QLORA_ERR_SHAPE;
+    for (int l = 0; l < kL; l++) {
+        QLORA_TRY(check_weight(&b->w[l]));
+        if (!aligned16(b->A[l]) || !aligned16(b->B[l])) return QLORA_ERR_ALIGNMENT;
+    }
+    Ctx c{b, layout_cached(b, kv->tokens, attn), static_cast<char *>(workspace), static_cast<cudaStream_t>(stream),
+          dev.sms};
+    if (workspace_bytes < c.L.bytes) return QLORA_ERR_WORKSPACE;
+    return forward_cached(c, cache, kv, rope, static_cast<const bf16 *>(x), static_cast<bf16 *>(y), window, sinks, attn);
+}
 
 extern "C" size_t qlora_block_workspace_bytes(const qlora_block *b)
 {

@@ -277,49 +277,61 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         }
     }
     __syncthreads();
-    // thread: piece i0 of every stride-th head, counted over the block's tokens
+    // thread: piece i0 of every stride-th head, counted over the block's tokens; two at a time, so
+    // that four loads are on their way
     const int per_token = p.heads + 2 * p.kv_heads, lanes = kAppendThreads / groups;
     const int i0 = ((int)threadIdx.x % groups) * 8, stride = lanes * (int)gridDim.y;
     if ((int)threadIdx.x >= lanes * groups) return;
     const int64_t slots = (int64_t)p.num_pages << p.page_shift;
     int head = blockIdx.y * lanes + (int)threadIdx.x / groups, tk = 0;
-    for (;; head += stride) {
-        while (head >= per_token) {
-            head -= per_token;
-            tk++;
-        }
-        if (tk >= toks) break;
-        const int64_t slot = slot_of[tk], t = t0 + tk;
-        if (slot < 0 || slot >= slots) continue;   // padding, a refused request, or not a place of the cache
-        const uint16_t *src;
-        uint16_t *dst;
-        bool rotate = p.rotate;
-        if (head < p.heads) {
-            const int64_t o = (t * p.heads + head) * p.head_dim;
-            src = p.q + o;
-            dst = p.q_out + o;
-        } else {
-            const bool is_v = head >= p.heads + p.kv_heads;
-            const int h = head - p.heads - (is_v ? p.kv_heads : 0);
-            src = (is_v ? p.v : p.k) + (t * p.kv_heads + h) * p.head_dim;
-            dst = (is_v ? p.vc : p.kc) + (slot >> p.page_shift) * p.stride_page + h * p.stride_head +
-                  (slot & ((1 << p.page_shift) - 1)) * p.stride_token;
-            if (is_v) rotate = false;
-        }
-        uint4 a = *reinterpret_cast<const uint4 *>(src + i0), b = *reinterpret_cast<const uint4 *>(src + i0 + half);
-        if (rotate) {
-            const float2 *tab = cs + tk * half + (i0 >> 3);
-            uint32_t *pa = reinterpret_cast<uint32_t *>(&a), *pb = reinterpret_cast<uint32_t *>(&b);
+    while (tk < toks) {
+        uint4 lo[2], hi[2];
+        uint16_t *dst[2];
+        const float2 *tab[2];   // null: no rotation
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float2 x = up2<F16>(pa[j]), y = up2<F16>(pb[j]);
-                const float2 c0 = tab[2 * j * groups], c1 = tab[(2 * j + 1) * groups];
-                pa[j] = down2<F16>(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
-                pb[j] = down2<F16>(x.x * c0.y + y.x * c0.x, x.y * c1.y + y.y * c1.x);
+        for (int n = 0; n < 2; n++, head += stride) {
+            while (head >= per_token) {
+                head -= per_token;
+                tk++;
             }
+            dst[n] = nullptr;
+            if (tk >= toks) continue;
+            const int64_t slot = slot_of[tk], t = t0 + tk;
+            if (slot < 0 || slot >= slots) continue;   // padding, a refused request, or not a place of the cache
+            const uint16_t *src;
+            tab[n] = p.rotate ? cs + tk * half + (i0 >> 3) : nullptr;
+            if (head < p.heads) {
+                const int64_t o = (t * p.heads + head) * p.head_dim;
+                src = p.q + o;
+                dst[n] = p.q_out + o;
+            } else {
+                const bool is_v = head >= p.heads + p.kv_heads;
+                const int h = head - p.heads - (is_v ? p.kv_heads : 0);
+                src = (is_v ? p.v : p.k) + (t * p.kv_heads + h) * p.head_dim;
+                dst[n] = (is_v ? p.vc : p.kc) + (slot >> p.page_shift) * p.stride_page + h * p.stride_head +
+                         (slot & ((1 << p.page_shift) - 1)) * p.stride_token;
+                if (is_v) tab[n] = nullptr;
+            }
+            lo[n] = *reinterpret_cast<const uint4 *>(src + i0);
+            hi[n] = *reinterpret_cast<const uint4 *>(src + i0 + half);
         }
-        *reinterpret_cast<uint4 *>(dst + i0) = a;
-        *reinterpret_cast<uint4 *>(dst + i0 + half) = b;
+#pragma unroll
+        for (int n = 0; n < 2; n++) {
+            if (!dst[n]) continue;
+            uint4 a = lo[n], b = hi[n];
+            if (tab[n]) {
+                uint32_t *pa = reinterpret_cast<uint32_t *>(&a), *pb = reinterpret_cast<uint32_t *>(&b);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float2 x = up2<F16>(pa[j]), y = up2<F16>(pb[j]);
+                    const float2 c0 = tab[n][2 * j * groups], c1 = tab[n][(2 * j + 1) * groups];
+                    pa[j] = down2<F16>(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
+                    pb[j] = down2<F16>(x.x * c0.y + y.x * c0.x, x.y * c1.y + y.y * c1.x);
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst[n] + i0) = a;
+            *reinterpret_cast<uint4 *>(dst[n] + i0 + half) = b;
+        }
     }
 }
 

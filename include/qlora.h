@@ -646,6 +646,30 @@ QLORA_API qlora_status qlora_paged_attn_fwd(const qlora_kv_cache *cache, const q
                                             int32_t heads, float scale, int32_t window, int32_t sinks, void *out,
                                             float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * qlora_block_fwd_cached -- the serving form of the block: y = block(x) for the
+ * new tokens of a planned batch, with attention over the layer's cache, to
+ * which their keys and values are appended (qlora_kv_append, then
+ * qlora_paged_attn_fwd).  The tokens of a request given in any chunks produce
+ * the rows of qlora_block_fwd over the whole sequence, up to rounding.
+ *   blk        as for qlora_block_fwd; batch, seq and rope_base are not used.
+ *   cache      this layer's, kv_heads = heads, the block's head_dim, QLORA_BF16.
+ *   kv         filled by qlora_kv_plan, once for all layers of the step; `rope`
+ *              as from qlora_build_rope.
+ *   x, y       device bf16 [kv->tokens, hidden].  Rows of y at and after
+ *              cu_q[batch], and those of refused requests, are unspecified.
+ *   window, sinks  as for qlora_paged_attn_fwd.
+ *   workspace  device, >= qlora_block_cached_workspace_bytes (0 for an invalid
+ *              description).
+ * Errors: INVALID_ARG, SHAPE, ALIGNMENT, WORKSPACE, CUDA, UNSUPPORTED.
+ */
+QLORA_API size_t qlora_block_cached_workspace_bytes(const qlora_block *blk, const qlora_kv_cache *cache,
+                                                    const qlora_kv_batch *kv);
+QLORA_API qlora_status qlora_block_fwd_cached(const qlora_block *blk, const qlora_kv_cache *cache,
+                                              const qlora_kv_batch *kv, const qlora_rope *rope, const void *x, void *y,
+                                              int32_t window, int32_t sinks, void *workspace, size_t workspace_bytes,
+                                              void *stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 QLORA_API const char *qlora_status_string(qlora_status status);
 
