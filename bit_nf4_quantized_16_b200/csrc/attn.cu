@@ -27,9 +27,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     const BatchView &v = p.v;
     const Desc d = p.desc[blockIdx.x];
     if (d.parts == 0) return;
-    const Request r = load_request(v, d.b);
-    const int row0 = blockIdx.y * 8;
-    const int rows = min(min(r.qn * v.group - d.rt * ROWS, ROWS) - row0, 8);
+    const int row0 = blockIdx.y * 8, rows = min(d.rows - row0, 8);
     if (rows <= 0) return;
     const int rp = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8, share = 8 / rp;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -69,8 +67,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     }
     if (row >= rows) return;
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    const int g = d.rt * ROWS + row0 + row, tok = v.token_of(g);
-    const int64_t orow = (int64_t)(r.q0 + tok) * v.heads + d.h * v.group + g - tok * v.group;
+    const int g = d.row0 + row0 + row, tok = v.token_of(g);
+    const int64_t orow = (int64_t)(d.q0 + tok) * v.heads + d.h * v.group + g - tok * v.group;
     const int64_t at = orow * v.head_dim + lane * V;
     if (lane * V < v.head_dim && QLORA_IN(at + V - 1, (int64_t)v.tokens * v.heads * v.head_dim)) {
         uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + at);
@@ -94,15 +92,14 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const __grid_constant
     const BatchView &v = p.v;
     const Desc d = p.desc[blockIdx.x];
     if (d.parts == 0) return;
-    const Request r = load_request(v, d.b);
-    const int row0 = blockIdx.y * 32, rows = min(min(r.qn * v.group - d.rt * ROWS, ROWS) - row0, 32);
+    const int row0 = blockIdx.y * 32, rows = min(d.rows - row0, 32);
     if (rows <= 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int64_t kSlot = ChunkCfg<DP>::kSlotFloats;
     auto slot = [&](int i) { return p.part + (i == 0 ? d.first_slot : 2 * (d.cta + i)) * kSlot; };
     auto tensor_row = [&](int row) {
-        const int g = d.rt * ROWS + row0 + row, t = v.token_of(g);
-        return (int64_t)(r.q0 + t) * v.heads + d.h * v.group + g - t * v.group;
+        const int g = d.row0 + row0 + row, t = v.token_of(g);
+        return (int64_t)(d.q0 + t) * v.heads + d.h * v.group + g - t * v.group;
     };
     if (lane < rows) {
         float M = -INFINITY, L = 0.0f;

@@ -177,7 +177,7 @@ struct ChunkItem {
     int pos0;         // position of the request's first row
     int whole, begins;
     Half half[2];
-    int b, rt, parts;
+    int parts;
 };
 
 struct ChunkBars {
@@ -320,8 +320,6 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                         o.begins = it.begins;
                         o.half[0] = half_of(v, it, 0);
                         o.half[1] = half_of(v, it, 1);
-                        o.b = it.b;
-                        o.rt = it.rt;
                         o.parts = it.begins ? cta_of_last(it.end, G, total) - (int)cta + 1 : 0;
                     }
                     mbar_arrive(&bars->item_full[items & 3]);
@@ -703,7 +701,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
             } else if (valid && p.lse) {
                 p.lse[orow] = l > 0.0f ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
             }
-            if (it->begins && threadIdx.x == 0) p.desc[cta] = Desc{it->b, it->h, it->rt, slot, (int)cta, it->parts};
+            if (it->begins && threadIdx.x == 0) p.desc[cta] = Desc{it->q0, it->h, it->row0, it->half[0].rows + it->half[1].rows, slot, (int)cta, it->parts};
             tiles += it->t1 - it->t0;
             tc_fence_before();   // these reads of O come before the next item's first product, behind p_ready
             __syncwarp();

@@ -43,7 +43,8 @@ struct BatchView {
 // last (slot 2c + 1).  A slot holds ROWS x DP outputs, ROWS maxima (of the
 // scores times scale * log2 e) and ROWS sums, all fp32.
 struct Desc {
-    int32_t b, h, rt;
+    int32_t q0, h;        // of the item: the request's first row, the key/value head,
+    int32_t row0, rows;   // its first row in the request and how many it has
     int32_t first_slot;   // of the item's first part; the next ones are 2 (c + 1), 2 (c + 2), ...
     int32_t cta, parts;   // parts = 0: this CTA begins no split item
 };

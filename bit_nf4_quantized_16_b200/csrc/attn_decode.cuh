@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
             }
         }
         if (it.begins && threadIdx.x == 0)
-            p.desc[cta] = Desc{it.b, it.h, it.rt, slot, (int)cta, cta_of_last(it.end, G, total) - (int)cta + 1};
+            p.desc[cta] = Desc{it.r.q0, it.h, it.rt * C::kRows, rows, slot, (int)cta, cta_of_last(it.end, G, total) - (int)cta + 1};
         __syncthreads();
     }
 }
