@@ -150,20 +150,61 @@ int decode_grid(const DeviceInfo &d) { return 2 * d.sms; }
 
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
+// CTAs per key/value head of the cluster form, or 0: not used.  The form gives
+// every head of every request the same number of CTAs, whatever the lengths are (the
+// host does not know them).  It saves 4 to 5 us a call where the requests are alike (4
+// requests of 3000 positions, 8 heads of 128: 13.5 us for 17.4; 500 positions of one request
+// with 32 heads: 6.8 for 11.2; 30000: 77 for 83) and loses up to 6 where they are not
+// (8 requests of 100 to 4000 positions: 23.7 for 17.4).  So it is taken for one
+// request alone that fills the device, and otherwise where a CTA reads few positions:
+// at most kWindowed under a window, which evens the lengths out (32 requests,
+// window 1024: 29.3 us for 34.6), or kOpen without one.
+constexpr int64_t kWindowed = 1280, kOpen = 640;
+int cluster_ctas(const AttnParams &p, const DeviceInfo &dev)
+{
+    const int64_t items = (int64_t)p.v.batch * p.v.kv_heads;
+    int n = 8;
+    while (n && n * items > decode_grid(dev)) n /= 2;
+    if (!n) return 0;
+    if (p.v.batch == 1 && n * items >= decode_grid(dev) / 2) return n;
+    const int64_t table = (int64_t)p.v.max_pages << p.v.page_shift;   // positions of a request, at most
+    const bool few = table <= kOpen * n || (p.v.window > 0 && (int64_t)p.v.window + p.v.sinks <= kWindowed * n);
+    return few ? n : 0;
+}
+
 template <int DP, bool F16>
 qlora_status launch_decode(AttnParams &p, const DeviceInfo &dev, cudaStream_t s)
 {
     using C = DecodeCfg<DP>;
     static PerDeviceOnce once;
     QLORA_TRY(once.run(dev.device, [] {
-        QLORA_CUDA_TRY(cudaFuncSetAttribute(decode_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        QLORA_CUDA_TRY(cudaFuncSetAttribute(decode_kernel<DP, F16, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            C::kBytes));
+        QLORA_CUDA_TRY(cudaFuncSetAttribute(decode_kernel<DP, F16, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                             C::kBytes));
         return QLORA_OK;
     }));
+    if (const int n = cluster_ctas(p, dev)) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(n * p.v.batch * p.v.kv_heads);
+        cfg.blockDim = dim3(C::kThreads);
+        cfg.dynamicSmemBytes = C::kBytes;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim = {(unsigned)n, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        LaunchScope ls(QLORA_KERNEL_ATTENTION, s);
+        QLORA_CUDA_TRY(cudaLaunchKernelEx(&cfg, decode_kernel<DP, F16, true>, p));
+        return launch_status();
+    }
     const int grid = decode_grid(dev);
     {
         LaunchScope ls(QLORA_KERNEL_ATTENTION, s);
-        QLORA_CUDA_TRY(launch_pdl(decode_kernel<DP, F16>, dim3(grid), dim3(C::kThreads), C::kBytes, s, p));
+        QLORA_CUDA_TRY(launch_pdl(decode_kernel<DP, F16, false>, dim3(grid), dim3(C::kThreads), C::kBytes, s, p));
     }
     {
         LaunchScope ls(QLORA_KERNEL_ATTENTION, s);

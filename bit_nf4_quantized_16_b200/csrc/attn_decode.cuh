@@ -15,6 +15,8 @@
 // pairs (p - hi is exact, lo rounds it at 2^-9 (bf16) of 2^-9): with a single
 // 16-bit p the output would carry its rounding beside the output's own.
 #pragma once
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace qlora {
@@ -67,11 +69,57 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DP, bool F16>
+// The walk of a CTA whose cluster has one key/value head of one request: an
+// equal share of the tiles of each of its row tiles (mostly there is one).
+template <int ROWS, int TILE>
+struct OneHead {
+    int b, h, rt, n_rt, rank, ranks;
+    Request r;
+
+    __device__ __forceinline__ void init(const BatchView &v)
+    {
+        rank = (int)sm100::cluster_ctarank();
+        ranks = (int)sm100::cluster_nctarank();
+        h = blockIdx.x / ranks;
+        b = h / v.kv_heads;
+        h -= b * v.kv_heads;
+        rt = 0;
+        r = load_request(v, b);
+        n_rt = row_tiles<ROWS>(v, r);
+    }
+    __device__ __forceinline__ bool next(const BatchView &v, Item &it)
+    {
+        if (rt >= n_rt) return false;
+        it.b = b;
+        it.h = h;
+        it.rt = rt;
+        it.r = r;
+        it.tiles = item_tiles<ROWS, TILE>(v, r, rt);
+        it.t0 = (int)((int64_t)it.tiles.n * rank / ranks);
+        it.t1 = (int)((int64_t)it.tiles.n * (rank + 1) / ranks);
+        it.whole = it.begins = false;
+        it.end = 0;
+        rt++;
+        return true;
+    }
+};
+
+__device__ __forceinline__ float ld_dsmem_f1(uint32_t addr)
+{
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+
+// CLUSTER: few items.  Every key/value head of every request has a cluster of CTAs
+// (of one to eight), which divide its keys and join their results through
+// distributed shared memory: no schedule to scan, no partial results in memory and
+// no second kernel.
+template <int DP, bool F16, bool CLUSTER>
 __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(const __grid_constant__ AttnParams p)
 {
     using C = DecodeCfg<DP>;
-    using W = Walker<C::kThreads, C::kRows, C::kTile, C::kOv>;
+    using W = std::conditional_t<CLUSTER, OneHead<C::kRows, C::kTile>, Walker<C::kThreads, C::kRows, C::kTile, C::kOv>>;
     using namespace sm100;
     constexpr int ST = C::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -95,17 +143,22 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
     }
     pdl_wait();
     pdl_trigger();
-    schedule_scan<C::kThreads, C::kRows, C::kTile, C::kOv>(v, pre);
-    const int64_t total = pre[C::kThreads];
-    const int64_t G = min((int64_t)gridDim.x, total), cta = blockIdx.x;
-    if (threadIdx.x == 0) p.desc[cta].parts = 0;
-    if (cta >= G) return;
-    const int64_t from = first_unit(cta, G, total), to = first_unit(cta + 1, G, total);
+    const int64_t cta = blockIdx.x;
+    int64_t G = 0, total = 0;
+    W wp, wc;   // the producer's walk, and the consumer's
+    if constexpr (CLUSTER) {
+        wp.init(v);
+    } else {
+        schedule_scan<C::kThreads, C::kRows, C::kTile, C::kOv>(v, pre);
+        total = pre[C::kThreads];
+        G = min((int64_t)gridDim.x, total);
+        if (threadIdx.x == 0) p.desc[cta].parts = 0;
+        if (cta >= G) return;
+        wp.init(v, pre, first_unit(cta, G, total), first_unit(cta + 1, G, total));
+    }
+    wc = wp;
 
     // ---- producer: one 16-position step of the next item that has any ----
-    W wp, wc;   // the producer's walk, and the consumer's
-    wp.init(v, pre, from, to);
-    wc = wp;
     Item pi;
     bool p_more = wp.next(v, pi);
     int pt = p_more ? pi.t0 : 0, p_item = 0, produced = 0, cache_t = -64, cache_page = -1;
@@ -338,6 +391,68 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
             stat[warp * 32 + 16 + rb] = l_b;
         }
         __syncthreads();
+        if constexpr (CLUSTER) {
+            // this CTA's joined rows over warp 0's, its maxima and sums over warp 0's
+            for (int i = threadIdx.x; i < rows * (DP / 4); i += C::kThreads) {
+                const int r = i / (DP / 4), c = (i % (DP / 4)) * 4;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < C::kWarps; w++) M = fmaxf(M, stat[w * 32 + r]);
+                float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int w = 0; w < C::kWarps; w++) {
+                    const float mw = stat[w * 32 + r], f = mw == -INFINITY ? 0.0f : exp2f(mw - M);
+                    const float4 x = *reinterpret_cast<const float4 *>(merge + (w * 16 + r) * C::kLd + c);
+                    a.x += f * x.x;
+                    a.y += f * x.y;
+                    a.z += f * x.z;
+                    a.w += f * x.w;
+                }
+                *reinterpret_cast<float4 *>(merge + r * C::kLd + c) = a;   // only this thread has read it
+            }
+            __syncthreads();
+            if (threadIdx.x < 16) {
+                const int r = threadIdx.x;
+                float M = -INFINITY, L = 0.0f;
+#pragma unroll
+                for (int w = 0; w < C::kWarps; w++) M = fmaxf(M, stat[w * 32 + r]);
+#pragma unroll
+                for (int w = 0; w < C::kWarps; w++) {
+                    const float mw = stat[w * 32 + r];
+                    L += mw == -INFINITY ? 0.0f : exp2f(mw - M) * stat[w * 32 + 16 + r];
+                }
+                stat[r] = M;
+                stat[16 + r] = L;
+            }
+            cluster_sync();
+            const uint32_t merge_at = smem_u32(merge), stat_at = smem_u32(stat);
+            [[maybe_unused]] const int64_t out_n = (int64_t)v.tokens * v.heads * v.head_dim;
+            for (int i = wc.rank * C::kThreads + threadIdx.x; i < rows * (DP / 4); i += wc.ranks * C::kThreads) {
+                const int r = i / (DP / 4), c = (i % (DP / 4)) * 4;
+                float M = -INFINITY, L = 0.0f;
+                for (int k = 0; k < wc.ranks; k++) M = fmaxf(M, ld_dsmem_f1(mapa_shared(stat_at + 4 * r, k)));
+                float4 a = make_float4(0, 0, 0, 0);
+                for (int k = 0; k < wc.ranks; k++) {
+                    const float m = ld_dsmem_f1(mapa_shared(stat_at + 4 * r, k)), f = m == -INFINITY ? 0.0f : exp2f(m - M);
+                    L += f * ld_dsmem_f1(mapa_shared(stat_at + 4 * (16 + r), k));
+                    const float4 x = ld_dsmem_f4(mapa_shared(merge_at + 4 * (r * C::kLd + c), k));
+                    a.x += f * x.x;
+                    a.y += f * x.y;
+                    a.z += f * x.z;
+                    a.w += f * x.w;
+                }
+                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+                const int g = gr0 + r, t = v.token_of(g);
+                const int64_t row = (int64_t)(it.r.q0 + t) * v.heads + it.h * v.group + g - t * v.group;
+                const int64_t at = row * v.head_dim + c;
+                if (c < v.head_dim && QLORA_IN(at + 3, out_n))
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
+                        make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
+                if (c == 0 && p.lse) p.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.69314718056f : -INFINITY;
+            }
+            cluster_sync();   // the others have read this CTA's results
+            continue;
+        }
         const int slot = 2 * (int)cta + (item == 0 ? 0 : 1);
         float *part = p.part + (int64_t)slot * C::kSlotFloats;
         [[maybe_unused]] const int64_t out_n = (int64_t)v.tokens * v.heads * v.head_dim;

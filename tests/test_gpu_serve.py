@@ -172,6 +172,34 @@ def test_one_long_request_is_split(q, heads, kv_heads, n):
     assert torch.equal(c.run().out, first)      # the same bits again
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (16, 1), (5, 5), (32, 32), (64, 64), (100, 100), (200, 200)])
+@pytest.mark.parametrize("kv,n,window,sinks", [(1000, 1, 0, 0), (1, 1, 0, 0), (70, 1, 0, 0), (4000, 1, 500, 3)])
+def test_one_request_alone(q, heads, kv_heads, kv, n, window, sinks):
+    """Clusters of CTAs per key/value head, down to none for many heads."""
+    Case(q, [kv], [n], heads, kv_heads, 64, 16, seed=50).run(window, sinks).check(window, sinks)
+
+
+@pytest.mark.parametrize("D", [16, 48, 128])
+@pytest.mark.parametrize("kv,n", [(0, 1), (0, 0), (3, 8), (90, 8), (2000, 3)])
+def test_one_request_alone_lengths(q, D, kv, n):
+    c = Case(q, [kv], [n], 4, 2, D, 32, torch.float16, seed=51, pad=9 - n)
+    first = c.run().check().out.clone()
+    assert torch.equal(c.run().out, first)
+
+
+@pytest.mark.parametrize("kv_heads,window,sinks", [(1, 0, 0), (4, 0, 0), (9, 100, 5), (25, 0, 0)])
+def test_few_requests(q, kv_heads, window, sinks):
+    """Clusters of eight, four, two and one CTAs per key/value head of eight requests."""
+    Case(q, [0, 1, 16, 65, 300, 700, 1000, 1200], [1, 0, 1, 1, 2, 1, 1, 1], 2 * kv_heads, kv_heads, 64, 16,
+         seed=54).run(window, sinks).check(window, sinks)
+
+
+def test_one_request_with_more_rows_than_promised(q):
+    """max_q_len only steers the choice of kernel."""
+    Case(q, [150], [30], 4, 2, 64, 16, seed=52, max_q_len=1).run().check()
+    Case(q, [150, 40], [30, 9], 4, 2, 64, 16, seed=53, max_q_len=1).run().check()
+
+
 def test_many_requests(q):
     rng = np.random.default_rng(6)
     lens = rng.integers(0, 200, 1300).tolist()
