@@ -577,28 +577,61 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 if (!ok) break;
                 n_s ^= 1;
                 tc_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; c++) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);
                 const uint32_t bad = bars->bad[(tiles + t - it->t0) & 7];
-                const bool all_seen = inside && bad == 0;
-                tmem_ld_wait();
-                if (!all_seen) {
-                    // columns [0, up) are not after the row; of them [0, front) are sinks and [low, up) in the window
+                if (!inside || bad) {
+                    // columns [0, up) are not after the row; of them [0, front) are sinks and [low, up) in
+                    // the window.  Masked in tensor memory, 32 columns at a time: done on the registers
+                    // below, the code (6 KB, run by one tile in three under a window) came
+                    // from far caches each time and cost as much as the tile's exponentials.
                     const int up = pos - tok0 + 1, low = v.window > 0 ? pos - v.window + 1 - tok0 : 0, front = v.sinks - tok0;
-#pragma unroll
+#pragma unroll 1
                     for (int g = 0; g < 4; g++) {
                         uint32_t seen = bits_below(up - 32 * g) & (~bits_below(low - 32 * g) | bits_below(front - 32 * g));
                         if ((bad >> (2 * g)) & 1u) seen &= 0xffff0000u;
                         if ((bad >> (2 * g + 1)) & 1u) seen &= 0x0000ffffu;
+                        if (!__any_sync(0xffffffffu, seen != ~0u)) continue;
+                        uint32_t x[2][16];
+                        tmem_ld_x16(s_addr + 32 * g, x[0]);
+                        tmem_ld_x16(s_addr + 32 * g + 16, x[1]);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 32; c++)
-                            if (!((seen >> c) & 1u)) s[g][c] = 0xff800000u;
+                        for (int c = 0; c < 32; c++) x[c >> 4][c & 15] = seen & (1u << c) ? x[c >> 4][c & 15] : 0xff800000u;
+                        tmem_st_x16(s_addr + 32 * g, x[0]);
+                        tmem_st_x16(s_addr + 32 * g + 16, x[1]);
                     }
+                    tmem_st_wait();
                 }
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; c++) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);
+                tmem_ld_wait();
                 float sum;
-                auto weights = [&]() {
-                    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), shift2 = pair(-m, -m);
+                bool again = t == t_first;   // find a reference first
+#pragma unroll 1
+                for (;;) {
+                    if (again) {
+                        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < 128; c++) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c >> 5][c & 31]));
+                        const float nm = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2);
+                        if (t > t_first) {
+                            // the product of the tile before is complete (this S came after it)
+                            const float fac = nm == -INFINITY ? 1.0f : ex2(m - nm);
+                            l *= fac;
+#pragma unroll 1
+                            for (int c = 0; c < DP / 16; c++) {
+                                uint32_t o[16];
+                                tmem_ld_x16(o_addr + 16 * c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
+                                tmem_st_x16(o_addr + 16 * c, o);
+                            }
+                        }
+                        m = nm;
+                    }
+                    const float shift = m == -INFINITY ? 0.0f : -m;   // against 0, all weights of a row without a key are 0
+                    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), shift2 = pair(shift, shift);
                     uint64_t sums[2] = {0, 0};
 #pragma unroll
                     for (int g = 0; g < 4; g++) {
@@ -614,34 +647,9 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                     }
                     const float2 total = unpair(add2(sums[0], sums[1]));
                     sum = total.x + total.y;
-                };
-                bool again = t == t_first;
-                if (!again) {
-                    weights();
-                    again = !(sum <= 32768.0f) || m == -INFINITY;
-                }
-                if (__any_sync(0xffffffffu, again)) {
-                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < 128; c++) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c >> 5][c & 31]));
-                    const float nm = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2);
-                    if (t > t_first) {
-                        // the product of the tile before is complete (this S came after it)
-                        const float fac = nm == -INFINITY ? 1.0f : ex2(m - nm);
-                        l *= fac;
-#pragma unroll 1
-                        for (int c = 0; c < DP / 16; c++) {
-                            uint32_t o[16];
-                            tmem_ld_x16(o_addr + 16 * c, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
-                            tmem_st_x16(o_addr + 16 * c, o);
-                        }
-                    }
-                    m = nm == -INFINITY ? 0.0f : nm;   // against 0, all weights of a row without a key are 0
-                    weights();
-                    m = nm;
+                    if (again) break;
+                    again = __any_sync(0xffffffffu, !(sum <= 32768.0f) || m == -INFINITY);
+                    if (!again) break;
                 }
                 l += sum;
                 tmem_st_wait();
