@@ -15,7 +15,7 @@
 // call needs no copy to the host, can be captured in a graph, and balances
 // requests of any mix of lengths.  A CTA whose part of an item is not the whole
 // item writes a partial result (unnormalized output, running maximum, sum);
-// combine_kernel joins the parts in the order of their CTAs.  The cut depends
+// a second kernel joins the parts in the order of their CTAs.  The cut depends
 // on the lengths and the device alone, so results are bitwise reproducible.
 #pragma once
 #include <cuda.h>
@@ -40,8 +40,9 @@ struct BatchView {
 };
 
 // A CTA's partial results: at most two, of its first item (slot 2c) and of its
-// last (slot 2c + 1).  A slot holds ROWS x DP outputs, ROWS maxima (of the
-// scores times scale * log2 e) and ROWS sums, all fp32.
+// last (slot 2c + 1).  A slot holds ROWS x DP outputs (in the kernel of many rows
+// four columns of all rows together, so that a warp of rows writes whole lines),
+// ROWS maxima (of the scores times scale * log2 e) and ROWS sums, all fp32.
 struct Desc {
     int32_t q0, h;        // of the item: the request's first row, the key/value head,
     int32_t row0, rows;   // its first row in the request and how many it has

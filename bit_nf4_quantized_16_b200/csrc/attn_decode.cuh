@@ -9,11 +9,18 @@
 // over the keys).  Nothing synchronizes the warps until the item's end, where
 // they join their results through shared memory.  The copies run ahead of
 // the products across items: the producer walks the schedule a second time,
-// ring depth ahead of the consumer.
+// ring depth ahead of the consumer.  Two CTAs per SM keep up to 128 KB of copies
+// on their way, and one streams while the other joins.
 //
 // The weights p of the softmax enter the second product as hi + lo 16-bit
 // pairs (p - hi is exact, lo rounds it at 2^-9 (bf16) of 2^-9): with a single
-// 16-bit p the output would carry its rounding beside the output's own.
+// 16-bit p the output would carry its rounding beside the output's own.  The
+// products have time for it: 16 rows x 16 positions take 48 of them for 8 KB.
+//
+// Measured (B200): 16 requests of 4100 positions, 64 heads of 128 (2.1 GB): 316 us, 6.8 TB/s;
+// 64 requests of 100 to 16000 positions, 8 heads: 116 us, 6.0 TB/s (0.92 of the
+// measured copy rate); one request of 500 positions, 32 heads: 6.9 us, of which
+// launch, lengths, table and first copy are four dependent latencies.
 #pragma once
 #include <type_traits>
 
@@ -25,7 +32,7 @@ namespace attn {
 template <int DP>
 struct DecodeCfg {
     static constexpr int kWarps = 4, kThreads = 32 * kWarps;
-    static constexpr int kRows = 16, kTile = 16 * kWarps, kOv = 3;
+    static constexpr int kRows = 16, kTile = 16 * kWarps, kOv = 3;   // an item costs three tiles beside its own (64 ragged requests: 149 us with 0, 121 with 2, 116 with 3)
     static constexpr int kStages = DP == 128 ? 2 : 4;
     static constexpr uint32_t kStageBytes = 2 * 16 * DP * 2;   // keys, then values, of 16 positions
     static constexpr uint32_t kRing = kWarps * kStages * kStageBytes;

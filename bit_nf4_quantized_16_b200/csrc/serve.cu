@@ -29,6 +29,9 @@ namespace {
 // three dependent reads, two scans), so a small batch gets one small CTA and a large
 // one as many threads as a cluster has; a thread takes four neighbouring
 // tokens, which mostly share the search.
+// Measured (B200): 16 requests of one token 4.8 us (append_kernel, which only streams,
+// takes 2.6 at its smallest); 1000 requests with 20651 tokens, 5937 returned and 1308
+// taken pages 11.4 us, of which the scans are a third.
 
 struct PlanParams {
     const int32_t *ctx, *qlen;
@@ -220,7 +223,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
 //
 // A block takes kTok tokens: it forms their angles once in shared memory, then
 // its threads move 16-byte pieces (a low and a high one that rotate together)
-// of q, k and v.  Bound by memory: every value is read and written once.
+// of q, k and v.  Bound by memory: every value is read and written once.  The
+// angles lie so in shared memory that the threads of a warp read neighbours.
+// Measured (B200): 7983 tokens, 32 + 8 + 8 heads of 128 (196 MB): 37.5 us, 5.2 TB/s (0.80 of
+// the measured copy rate); 16 tokens of 3 x 64 heads: 2.6 us, latency.
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 8;   // at most, per block
