@@ -340,11 +340,14 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 }
                 items++;
                 if (!more) break;
+                // positions from the sinks to here: no row sees them
+                const int before = v.window > 0 ? it.r.kv - it.r.qn + v.token_of(it.rt * C::kRows) - v.window : -1;
                 for (int t = it.t0; ok && t < it.t1; t++, tiles++) {
                     const int tok0 = it.tiles.at(t) * 128, mine = tok0 + lane * box;
                     int page = v.num_pages;   // a page outside the cache: the copy fills zeros
                     bool bad = false;
-                    if (lane < pieces && mine < it.r.kv) {
+                    // (a page that no row sees may be another request's by now, or hold anything)
+                    if (lane < pieces && mine < it.r.kv && (mine < v.sinks || mine + box - 1 > before)) {
                         const int id = page_of(v, it.b, mine);
                         bad = id < 0;
                         if (id >= 0) page = id;

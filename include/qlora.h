@@ -624,8 +624,12 @@ QLORA_API qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora_
  *     out[t][h] = sum_j p_j v_j,  p = softmax over those j of scale * q[t][h] . k_j
  * with k, v of head h / (heads / kv_heads).  A row that sees nothing gets
  * zeros.  Positions whose table entry is no page of the cache, or that lie
- * beyond the table, are left out as if they were masked.  Rows of `out` at
- * and after cu_q[batch] are left as they were.
+ * beyond the table, are left out as if they were masked.  Under a window, pages
+ * (pieces of 128 positions of larger ones) of which no row sees a position are
+ * not used, whatever their entries say and they hold: a caller may have given
+ * them to another request.  Elsewhere a position that a row does not see has weight 0 in
+ * it; a value there that is not finite makes that NaN, as in any product.  Rows
+ * of `out` at and after cu_q[batch] are left as they were.
  *   q, out  device [tokens][heads][head_dim] of the cache's type, tokens *
  *           heads <= 2^30; out may not be q.
  *   scale   finite, above 0.

@@ -298,6 +298,19 @@ def test_chunk_positions_beyond_the_table_are_left_out(q):
     c.run().check(present=[np.arange(200) < 96, np.arange(90) < 96])
 
 
+@pytest.mark.parametrize("n,D,page", [(1, 64, 16), (1, 128, 128), (40, 64, 16), (40, 128, 64), (300, 128, 32)])
+@pytest.mark.parametrize("sinks", [0, 5, 140])
+def test_pages_that_no_row_sees_may_hold_anything(q, n, D, page, sinks):
+    """Pages between the sinks and the first row's window went back to the pool and hold NaN."""
+    window, lengths = 100, [1000, 700, 430]
+    c = Case(q, lengths, [n] * 3, 4, 2, D, page, seed=43)
+    for b, L in enumerate(lengths):
+        for i in range(-(-sinks // page), max(0, L - n - window + 1) // page):
+            page_id = int(c.table[b, i])
+            c.cache.k[page_id], c.cache.v[page_id] = math.nan, math.nan
+    c.run(window, sinks).check(window, sinks, rows=None if n < 100 else [0, 1, 99, 127, 128, 200, 299])
+
+
 def test_bad_pages_are_left_out(q):
     c = Case(q, [200, 90, 64], [1, 2, 1], 4, 2, 64, 16, seed=8)
     present = [np.ones(200, bool), np.ones(90, bool), np.zeros(64, bool)]
