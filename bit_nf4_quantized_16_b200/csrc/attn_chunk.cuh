@@ -31,7 +31,7 @@
 // each, averaged over the keys: the output's own rounding is as large); sums are
 // taken of the unrounded fp32 weights.
 //
-// Measured (B200, 1965 MHz).  2048 tokens over 16000 positions, 32 heads of 128: 530 to
+// Measured (B200, 1965 MHz; on another one at 1.66 GHz a prompt takes 177 us).  2048 tokens over 16000 positions, 32 heads of 128: 530 to
 // 550 us, 1030 to 1090 TFLOP/s (0.61 to 0.65 of the measured GEMM rate); a whole prompt of
 // 4096 tokens: 152 to 156 us; heads of 64: 650 TFLOP/s.  A tile of both halves takes 4080
 // cycles: its 32 products take 90 cycles each (2880; that is the GEMM rate), a half's softmax
@@ -41,7 +41,9 @@
 // at that time, and 169 for 157 later); S in steps of 64 columns with two buffers (184 for
 // 182, 221 with a group of warps for each buffer); a quarter of the exponentials by a
 // polynomial (215 for 182); signalling the first 64 weights early (174 for 170);
-// a transposing epilogue (163 for 157).
+// a transposing epilogue (163 for 157).  At heads of 64, which leave room: the weights in
+// columns of their own, so that the next S is formed during the softmax (ragged chunks
+// 66.5 to 69.2 for 61.2); two buffers of query rows (60.5 for 61.1).
 #pragma once
 #include "attn_common.cuh"
 
