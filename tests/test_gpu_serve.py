@@ -360,6 +360,43 @@ def test_another_stream(q):
     Case(q, [300, 40], [1, 1], 4, 2, 128, 16, seed=12).run(stream=torch.cuda.Stream()).check()
 
 
+@pytest.mark.parametrize("n,D", [(1, 64), (1, 128), (40, 64), (300, 128)])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_row_that_is_not_finite_stays_alone(q, n, D, value):
+    """One head of one token: every other row keeps its value, up to half a step of
+    itself and of the weights (on values of at most max |v|) in each of the two calls."""
+    c = Case(q, [700, 500], [n, n], 8, 2, D, 16, seed=44).run()
+    clean = c.out.float()
+    c.qt[n // 2, 5] = value
+    c.run()
+    others = torch.ones(c.T, 8, dtype=torch.bool, device="cuda")
+    others[n // 2, 5] = False
+    assert not torch.isfinite(c.out[n // 2, 5].float()).any()
+    top = max(float(v.float().abs().max()) for v in c.vd)
+    diff = (c.out.float() - clean).abs()
+    assert (diff <= 2.0 ** -7 * clean.abs() * (1 + 2.0 ** -7) + (2.0 ** -7 + 2.0 ** -16) * top)[others].all()
+
+
+def test_calls_at_once(q):
+    """Four calls on four streams, each with its workspace, over and over."""
+    cases = [Case(q, [900, 33], [1, 1], 8, 2, 128, 16, seed=45), Case(q, [900, 330], [70, 300], 8, 2, 128, 16, seed=46),
+             Case(q, [2000], [1], 32, 32, 64, 16, seed=47), Case(q, [600, 20], [200, 20], 8, 8, 64, 32, seed=48)]
+    calls = []
+    for c in cases:
+        c.run()
+        n = q.qlora_paged_attn_workspace_bytes(c.cache, c.kv, c.H)
+        calls.append((c, torch.cuda.Stream(), torch.full((n,), 0xff, dtype=torch.uint8, device="cuda"),
+                      torch.full_like(c.out, 7.0), torch.full_like(c.lse, 7.0)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, stream, ws, out, lse in calls:
+            q.qlora_paged_attn_fwd(c.cache, c.kv, c.qt, out, c.D ** -0.5, ws, lse=lse, stream=stream)
+    torch.cuda.synchronize()
+    q.qlora_check_device_error()
+    for c, _, _, out, lse in calls:     # the same call gives the same bits
+        assert torch.equal(out, c.out) and torch.equal(lse, c.lse)
+
+
 def test_captured_and_replayed_with_other_lengths(q):
     a = Case(q, [300, 40, 77], [1, 1, 1], 4, 2, 128, 16, seed=13, width=30)
     b = Case(q, [5, 470, 0], [1, 1, 1], 4, 2, 128, 16, seed=14, width=30)
