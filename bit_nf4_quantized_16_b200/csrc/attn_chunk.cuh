@@ -43,7 +43,7 @@
 // polynomial (215 for 182); signalling the first 64 weights early (174 for 170);
 // a transposing epilogue (163 for 157).  At heads of 64, which leave room: the weights in
 // columns of their own, so that the next S is formed during the softmax (ragged chunks
-// 66.5 to 69.2 for 61.2); two buffers of query rows (60.5 for 61.1).
+// 62 to 69, by where the softmax waits, for 61); two buffers of query rows (60.5 for 61.1).
 #pragma once
 #include "attn_common.cuh"
 
