@@ -15,7 +15,7 @@ namespace attn {
 
 // Joins the parts of one split item (block x: the CTA that begins it; block y:
 // eight of its rows).  One to eight warps share a row, each taking every
-// n-th part; parts are weighted by 2^(m_i - M) and summed in a fixed order.
+// n-th part; parts are weighted by 2^((m_i - M) scale log2 e) and summed in a fixed order.
 template <int ROWS, int DP, bool F16>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnParams p)
 {
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
         for (int i = sp; i < d.parts; i += share) {
             const float *s = slot(i);
             const float m = s[ROWS * DP + row0 + row];
-            const float f = m == -INFINITY ? 0.0f : exp2f(m - M);
+            const float f = m == -INFINITY ? 0.0f : exp2f((m - M) * p.scale_log2);
             L += f * s[ROWS * DP + ROWS + row0 + row];
             const float *x = s + (row0 + row) * DP + lane * V;
 #pragma unroll
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
 #pragma unroll
         for (int k = 0; k < V / 2; k++) o[k] = pack2<F16>(a[2 * k] * inv, a[2 * k + 1] * inv);
     }
-    if (lane == 0 && p.lse) p.lse[orow] = L > 0.0f ? (M + log2f(L)) * 0.69314718056f : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[orow] = L > 0.0f ? __fmaf_rn(M, p.scale_log2, log2f(L)) * 0.69314718056f : -INFINITY;
 }
 
 // The same for the items of the kernel of many rows: block y takes 32 rows, one
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const __grid_constant
 #pragma unroll 2
         for (int i = 0; i < d.parts; i++) {
             const float *s = slot(i) + row0 + lane;
-            const float m = s[ROWS * DP], f = m == -INFINITY ? 0.0f : exp2f(m - M);
+            const float m = s[ROWS * DP], f = m == -INFINITY ? 0.0f : exp2f((m - M) * p.scale_log2);
             L += f * s[ROWS * DP + ROWS];
 #pragma unroll
             for (int k = 0; k < DP / 32; k++) {
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < DP / 32; k++)
             rows_out[lane][8 * k + warp] = make_uint2(pack2<F16>(a[k].x * inv, a[k].y * inv), pack2<F16>(a[k].z * inv, a[k].w * inv));
-        if (warp == 0 && p.lse) p.lse[tensor_row(lane)] = L > 0.0f ? (M + log2f(L)) * 0.69314718056f : -INFINITY;
+        if (warp == 0 && p.lse) p.lse[tensor_row(lane)] = L > 0.0f ? __fmaf_rn(M, p.scale_log2, log2f(L)) * 0.69314718056f : -INFINITY;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (DP / 4); i += 256) {

@@ -63,6 +63,9 @@ struct ChunkCfg {
     static constexpr uint32_t kBytes = kBarOff + 1024 + 1024;   // + alignment slack
     static constexpr int kSlotFloats = kRows * DP + 2 * kRows;
     static constexpr uint32_t kOCol = 256;                 // O_A, O_B at 256 + DP * half; S at 128 * half
+    // From this size of a reference (in powers of two) on, scores lose their reference before they are scaled; below it
+    // the rounding of reference * scale, which is the same for all of a row's weights, moves them by 2^-9 at most.
+    static constexpr float kFar = 65536.0f;
     static constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;   // 2 * 200 + 104 = 3 * 168, the launch's share
 };
 
@@ -586,7 +589,8 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
             const int t_first = f.t.first, t_last = f.t.last;
             const bool valid = row < f.rows, has = f.t.has();
             const int pos = valid ? it->pos0 + v.token_of(it->row0 + h * 128 + row) : -1;
-            float m = valid ? -INFINITY : 0.0f, l = 0.0f;   // m: the reference of the weights, -inf: none yet
+            float m = valid ? -INFINITY : 0.0f, l = 0.0f;   // m: the reference of the weights, a score; -inf: none yet
+            bool far = false;                               // a row of this warp has one of kFar or more
             for (int t = t_first; t <= t_last; t++) {
                 if (!f.t.takes(t)) continue;
                 const int tok0 = it->tiles.at(t) * 128;
@@ -625,17 +629,17 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 for (int c = 0; c < 4; c++) tmem_ld_32x32b_x32(s_addr + 32 * c, s[c]);
                 tmem_ld_wait();
                 float sum;
-                bool again = t == t_first;   // find a reference first
+                bool again = t == t_first || far;   // find a reference first
 #pragma unroll 1
                 for (;;) {
                     if (again) {
                         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int c = 0; c < 128; c++) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c >> 5][c & 31]));
-                        const float nm = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2);
+                        const float nm = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
                         if (t > t_first) {
                             // the product of the tile before is complete (this S came after it)
-                            const float fac = nm == -INFINITY ? 1.0f : ex2(m - nm);
+                            const float fac = nm == -INFINITY ? 1.0f : ex2((m - nm) * p.scale_log2);
                             l *= fac;
 #pragma unroll 1
                             for (int c = 0; c < DP / 16; c++) {
@@ -648,8 +652,15 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                             }
                         }
                         m = nm;
+                        far = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * p.scale_log2) >= C::kFar);
                     }
-                    const float shift = m == -INFINITY ? 0.0f : -m;   // against 0, all weights of a row without a key are 0
+                    const float ref = m == -INFINITY ? 0.0f : m;   // against 0, all weights of a row without a key are 0
+                    float shift = -ref * p.scale_log2;
+                    if (far) {   // (only in a pass that has looked for the reference, so it is the last)
+                        shift = 0.0f;
+#pragma unroll
+                        for (int c = 0; c < 128; c++) s[c >> 5][c & 31] = __float_as_uint(__uint_as_float(s[c >> 5][c & 31]) - ref);
+                    }
                     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), shift2 = pair(shift, shift);
                     uint64_t sums[2] = {0, 0};
 #pragma unroll
@@ -726,7 +737,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 part[C::kRows * DP + pr] = m;
                 part[C::kRows * DP + C::kRows + pr] = l;
             } else if (valid && p.lse) {
-                p.lse[orow] = l > 0.0f ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
+                p.lse[orow] = l > 0.0f ? __fmaf_rn(m, p.scale_log2, log2f(l)) * 0.69314718056f : -INFINITY;
             }
             if (it->begins && threadIdx.x == 0) p.desc[cta] = Desc{it->q0, it->h, it->row0, it->half[0].rows + it->half[1].rows, slot, (int)cta, it->parts};
             tiles += it->t1 - it->t0;

@@ -42,7 +42,12 @@ struct BatchView {
 // A CTA's partial results: at most two, of its first item (slot 2c) and of its
 // last (slot 2c + 1).  A slot holds ROWS x DP outputs (in the kernel of many rows
 // four columns of all rows together, so that a warp of rows writes whole lines),
-// ROWS maxima (of the scores times scale * log2 e) and ROWS sums, all fp32.
+// ROWS references and ROWS sums, all fp32.
+//
+// References are scores: a weight is 2^((s - reference) * scale * log2 e).  The difference is
+// formed first, and with the largest score as reference it is 0 for that one, exactly.  (A product
+// rounded before the subtraction is off by up to half its step, which is 16 at 2^28: weights of 2^16 or
+// 2^-16 where the largest has to be 1.)
 struct Desc {
     int32_t q0, h;        // of the item: the request's first row, the key/value head,
     int32_t row0, rows;   // its first row in the request and how many it has

@@ -318,12 +318,10 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                 x_a = fmaxf(x_a, __shfl_xor_sync(0xffffffffu, x_a, d));
                 x_b = fmaxf(x_b, __shfl_xor_sync(0xffffffffu, x_b, d));
             }
-            x_a *= p.scale_log2;
-            x_b *= p.scale_log2;
             if (__any_sync(0xffffffffu, x_a > m_a || x_b > m_b)) {
                 const float n_a = fmaxf(m_a, x_a), n_b = fmaxf(m_b, x_b);
-                const float f_a = n_a == -INFINITY ? 1.0f : exp2f(m_a - n_a);
-                const float f_b = n_b == -INFINITY ? 1.0f : exp2f(m_b - n_b);
+                const float f_a = n_a == -INFINITY ? 1.0f : exp2f((m_a - n_a) * p.scale_log2);
+                const float f_b = n_b == -INFINITY ? 1.0f : exp2f((m_b - n_b) * p.scale_log2);
                 m_a = n_a;
                 m_b = n_b;
                 l_a *= f_a;
@@ -341,10 +339,10 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
             float w[2][4];
 #pragma unroll
             for (int n = 0; n < 2; n++) {
-                w[n][0] = exp2f(__fmaf_rn(sc[n][0], p.scale_log2, -u_a));
-                w[n][1] = exp2f(__fmaf_rn(sc[n][1], p.scale_log2, -u_a));
-                w[n][2] = exp2f(__fmaf_rn(sc[n][2], p.scale_log2, -u_b));
-                w[n][3] = exp2f(__fmaf_rn(sc[n][3], p.scale_log2, -u_b));
+                w[n][0] = exp2f((sc[n][0] - u_a) * p.scale_log2);
+                w[n][1] = exp2f((sc[n][1] - u_a) * p.scale_log2);
+                w[n][2] = exp2f((sc[n][2] - u_b) * p.scale_log2);
+                w[n][3] = exp2f((sc[n][3] - u_b) * p.scale_log2);
                 l_a += w[n][0] + w[n][1];
                 l_b += w[n][2] + w[n][3];
             }
@@ -408,7 +406,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                 float4 a = make_float4(0, 0, 0, 0);
 #pragma unroll
                 for (int w = 0; w < C::kWarps; w++) {
-                    const float mw = stat[w * 32 + r], f = mw == -INFINITY ? 0.0f : exp2f(mw - M);
+                    const float mw = stat[w * 32 + r], f = mw == -INFINITY ? 0.0f : exp2f((mw - M) * p.scale_log2);
                     const float4 x = *reinterpret_cast<const float4 *>(merge + (w * 16 + r) * C::kLd + c);
                     a.x += f * x.x;
                     a.y += f * x.y;
@@ -426,7 +424,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
 #pragma unroll
                 for (int w = 0; w < C::kWarps; w++) {
                     const float mw = stat[w * 32 + r];
-                    L += mw == -INFINITY ? 0.0f : exp2f(mw - M) * stat[w * 32 + 16 + r];
+                    L += mw == -INFINITY ? 0.0f : exp2f((mw - M) * p.scale_log2) * stat[w * 32 + 16 + r];
                 }
                 stat[r] = M;
                 stat[16 + r] = L;
@@ -440,7 +438,8 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                 for (int k = 0; k < wc.ranks; k++) M = fmaxf(M, ld_dsmem_f1(mapa_shared(stat_at + 4 * r, k)));
                 float4 a = make_float4(0, 0, 0, 0);
                 for (int k = 0; k < wc.ranks; k++) {
-                    const float m = ld_dsmem_f1(mapa_shared(stat_at + 4 * r, k)), f = m == -INFINITY ? 0.0f : exp2f(m - M);
+                    const float m = ld_dsmem_f1(mapa_shared(stat_at + 4 * r, k));
+                    const float f = m == -INFINITY ? 0.0f : exp2f((m - M) * p.scale_log2);
                     L += f * ld_dsmem_f1(mapa_shared(stat_at + 4 * (16 + r), k));
                     const float4 x = ld_dsmem_f4(mapa_shared(merge_at + 4 * (r * C::kLd + c), k));
                     a.x += f * x.x;
@@ -455,7 +454,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                 if (c < v.head_dim && QLORA_IN(at + 3, out_n))
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
                         make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-                if (c == 0 && p.lse) p.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.69314718056f : -INFINITY;
+                if (c == 0 && p.lse) p.lse[row] = L > 0.0f ? __fmaf_rn(M, p.scale_log2, log2f(L)) * 0.69314718056f : -INFINITY;
             }
             cluster_sync();   // the others have read this CTA's results
             continue;
@@ -474,7 +473,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
             float4 a = make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int w = 0; w < C::kWarps; w++) {
-                const float f = mw[w] == -INFINITY ? 0.0f : exp2f(mw[w] - M);
+                const float f = mw[w] == -INFINITY ? 0.0f : exp2f((mw[w] - M) * p.scale_log2);
                 const float4 x = *reinterpret_cast<const float4 *>(merge + (w * 16 + r) * C::kLd + c);
                 L += f * stat[w * 32 + 16 + r];
                 a.x += f * x.x;
@@ -490,7 +489,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                 if (c < v.head_dim && QLORA_IN(at + 3, out_n))
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
                         make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-                if (c == 0 && p.lse) p.lse[row] = L > 0.0f ? (M + log2f(L)) * 0.69314718056f : -INFINITY;
+                if (c == 0 && p.lse) p.lse[row] = L > 0.0f ? __fmaf_rn(M, p.scale_log2, log2f(L)) * 0.69314718056f : -INFINITY;
             } else {
                 *reinterpret_cast<float4 *>(part + r * DP + c) = a;
                 if (c == 0) {
