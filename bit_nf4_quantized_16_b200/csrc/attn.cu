@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
 #pragma unroll
         for (int k = 0; k < V / 2; k++) o[k] = pack2<F16>(a[2 * k] * inv, a[2 * k + 1] * inv);
     }
-    if (lane == 0 && p.lse) p.lse[orow] = L > 0.0f ? __fmaf_rn(M, p.scale_log2, log2f(L)) * 0.69314718056f : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[orow] = log_sum<kRaiseFew<F16>>(M, L, p.scale_log2);
 }
 
 // The same for the items of the kernel of many rows: block y takes 32 rows, one
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < DP / 32; k++)
             rows_out[lane][8 * k + warp] = make_uint2(pack2<F16>(a[k].x * inv, a[k].y * inv), pack2<F16>(a[k].z * inv, a[k].w * inv));
-        if (warp == 0 && p.lse) p.lse[tensor_row(lane)] = L > 0.0f ? __fmaf_rn(M, p.scale_log2, log2f(L)) * 0.69314718056f : -INFINITY;
+        if (warp == 0 && p.lse) p.lse[tensor_row(lane)] = log_sum<kRaiseMany<F16>>(M, L, p.scale_log2);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (DP / 4); i += 256) {

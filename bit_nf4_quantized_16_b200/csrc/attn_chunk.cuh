@@ -23,12 +23,14 @@
 // Softmax: one pass, with weights against a reference m that is the row's maximum
 // over its first tile and moves only when it has to.  Any reference gives the same
 // quotient as long as no weight leaves the 16-bit type's range, and the sum
-// of a tile's weights, which is needed anyway, tells: up to 2^15 none has.  So the
+// of a tile's weights, which is needed anyway, tells: up to kMost none has at the upper end (for
+// the lower one see kRaiseMany).  So the
 // maximum of a tile is not looked for at all, unless that sum is larger or the row
 // has had no reference yet; then the weights are formed again against the new
 // maximum, and the output is rescaled by the softmax threads before they are
 // handed over.  The weights are rounded to the operands' 16-bit type (half a step
-// each, averaged over the keys: the output's own rounding is as large); sums are
+// each, averaged over the keys: the output's own rounding is as large; fp16 weights below 2^-22 of the
+// row's largest, 2^-33 of that); sums are
 // taken of the unrounded fp32 weights.
 //
 // Measured (B200, 1965 MHz; on another one at 1.66 GHz a prompt takes 177 us).  2048 tokens over 16000 positions, 32 heads of 128: 530 to
@@ -246,6 +248,8 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
     using W = Walker<C::kThreads, C::kRows, C::kTile, C::kOv>;
     using namespace sm100;
     constexpr int ST = C::kStages;
+    constexpr float kRaise = kRaiseMany<F16>;
+    constexpr float kMost = F16 ? 65504.0f : 32768.0f;   // of a tile's sum: fp16's largest value, 2^15
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     ChunkBars *bars = reinterpret_cast<ChunkBars *>(smem + C::kBarOff);
@@ -655,9 +659,9 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                         far = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m * p.scale_log2) >= C::kFar);
                     }
                     const float ref = m == -INFINITY ? 0.0f : m;   // against 0, all weights of a row without a key are 0
-                    float shift = -ref * p.scale_log2;
+                    float shift = __fmaf_rn(-ref, p.scale_log2, kRaise);
                     if (far) {   // (only in a pass that has looked for the reference, so it is the last)
-                        shift = 0.0f;
+                        shift = kRaise;
 #pragma unroll
                         for (int c = 0; c < 128; c++) s[c >> 5][c & 31] = __float_as_uint(__uint_as_float(s[c >> 5][c & 31]) - ref);
                     }
@@ -678,7 +682,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                     const float2 total = unpair(add2(sums[0], sums[1]));
                     sum = total.x + total.y;
                     if (again) break;
-                    again = __any_sync(0xffffffffu, !(sum <= 32768.0f) || m == -INFINITY);
+                    again = __any_sync(0xffffffffu, !(sum <= kMost) || m == -INFINITY);
                     if (!again) break;
                 }
                 l += sum;
@@ -737,7 +741,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 part[C::kRows * DP + pr] = m;
                 part[C::kRows * DP + C::kRows + pr] = l;
             } else if (valid && p.lse) {
-                p.lse[orow] = l > 0.0f ? __fmaf_rn(m, p.scale_log2, log2f(l)) * 0.69314718056f : -INFINITY;
+                p.lse[orow] = log_sum<kRaiseMany<F16>>(m, l, p.scale_log2);
             }
             if (it->begins && threadIdx.x == 0) p.desc[cta] = Desc{it->q0, it->h, it->row0, it->half[0].rows + it->half[1].rows, slot, (int)cta, it->parts};
             tiles += it->t1 - it->t0;

@@ -48,6 +48,14 @@ struct BatchView {
 // formed first, and with the largest score as reference it is 0 for that one, exactly.  (A product
 // rounded before the subtraction is off by up to half its step, which is 16 at 2^28: weights of 2^16 or
 // 2^-16 where the largest has to be 1.)
+//
+// In fp16 all weights of a call carry a power of two more, 2^kRaise, which cancels in the quotient.
+// Below 2^-14 fp16 has a fixed step of 2^-24, so that with weights of at most 1 the many small ones beside a
+// key that takes nearly all weight would lose their bits (a key 2^20 above the others: 3 of 11
+// left, none at 2^25); above 1 the type has room that costs nothing.  With few rows the reference is the
+// largest score so far: 2^15.  With many rows it is the largest of the first tile, of whose 128
+// keys the sum has to stay in range: 2^8.  A weight is then off by half a step or by
+// 2^-40 (few rows) or 2^-33 (many) of the row's largest.  bf16 has the exponents of fp32.
 struct Desc {
     int32_t q0, h;        // of the item: the request's first row, the key/value head,
     int32_t row0, rows;   // its first row in the request and how many it has
@@ -67,6 +75,17 @@ struct AttnParams {
     int *err;
     uint64_t timeout_ns;
 };
+
+template <bool F16> constexpr int kRaiseFew = F16 ? 15 : 0;
+template <bool F16> constexpr int kRaiseMany = F16 ? 8 : 0;
+
+// log sum exp of a row from its reference and the sum of its weights.
+template <int RAISE>
+__device__ __forceinline__ float log_sum(float ref, float sum, float scale_log2)
+{
+    constexpr float kLower = 1.0f / (float)(1 << RAISE);
+    return sum > 0.0f ? __fmaf_rn(ref, scale_log2, log2f(sum * kLower)) * 0.69314718056f : -INFINITY;
+}
 
 struct Request {
     int q0, qn;   // rows of the batch's tensors [q0, q0 + qn)

@@ -13,7 +13,8 @@
 // on their way, and one streams while the other joins.
 //
 // The weights p of the softmax enter the second product as hi + lo 16-bit
-// pairs (p - hi is exact, lo rounds it at 2^-9 (bf16) of 2^-9): with a single
+// pairs: p - hi is exact, and lo rounds it, to 2^-18 of p in bf16, and in fp16 to 2^-22
+// of p or 2^-40 of the largest weight (see kRaiseFew).  With a single
 // 16-bit p the output would carry its rounding beside the output's own.  The
 // products have time for it: 16 rows x 16 positions take 48 of them for 8 KB.
 //
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
     using W = std::conditional_t<CLUSTER, OneHead<C::kRows, C::kTile>, Walker<C::kThreads, C::kRows, C::kTile, C::kOv>>;
     using namespace sm100;
     constexpr int ST = C::kStages;
+    constexpr float kRaise = kRaiseFew<F16>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t pre[C::kThreads + 1 + C::kWarps];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -339,10 +341,10 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
             float w[2][4];
 #pragma unroll
             for (int n = 0; n < 2; n++) {
-                w[n][0] = exp2f((sc[n][0] - u_a) * p.scale_log2);
-                w[n][1] = exp2f((sc[n][1] - u_a) * p.scale_log2);
-                w[n][2] = exp2f((sc[n][2] - u_b) * p.scale_log2);
-                w[n][3] = exp2f((sc[n][3] - u_b) * p.scale_log2);
+                w[n][0] = exp2f(__fmaf_rn(sc[n][0] - u_a, p.scale_log2, kRaise));
+                w[n][1] = exp2f(__fmaf_rn(sc[n][1] - u_a, p.scale_log2, kRaise));
+                w[n][2] = exp2f(__fmaf_rn(sc[n][2] - u_b, p.scale_log2, kRaise));
+                w[n][3] = exp2f(__fmaf_rn(sc[n][3] - u_b, p.scale_log2, kRaise));
                 l_a += w[n][0] + w[n][1];
                 l_b += w[n][2] + w[n][3];
             }
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                 if (c < v.head_dim && QLORA_IN(at + 3, out_n))
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
                         make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-                if (c == 0 && p.lse) p.lse[row] = L > 0.0f ? __fmaf_rn(M, p.scale_log2, log2f(L)) * 0.69314718056f : -INFINITY;
+                if (c == 0 && p.lse) p.lse[row] = log_sum<kRaiseFew<F16>>(M, L, p.scale_log2);
             }
             cluster_sync();   // the others have read this CTA's results
             continue;
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                 if (c < v.head_dim && QLORA_IN(at + 3, out_n))
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
                         make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-                if (c == 0 && p.lse) p.lse[row] = L > 0.0f ? __fmaf_rn(M, p.scale_log2, log2f(L)) * 0.69314718056f : -INFINITY;
+                if (c == 0 && p.lse) p.lse[row] = log_sum<kRaiseFew<F16>>(M, L, p.scale_log2);
             } else {
                 *reinterpret_cast<float4 *>(part + r * DP + c) = a;
                 if (c == 0) {

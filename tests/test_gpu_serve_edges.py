@@ -61,3 +61,42 @@ def test_scores_of_any_size(q, kv_len, q_len, heads, kv_heads, D, dtype, size): 
                     assert (np.abs(got - want) <= EPS[dtype] / 2 * np.abs(want)).all(), (b, i, h)
                     assert abs(lse[int(c.cu[b]) + i, h] - s[first]) <= off + 2.0 ** -20 * abs(s[first]) + 64, (b, i, h)
     assert sure * 2 > sum(q_len) * heads      # most rows have such a key
+
+
+@pytest.mark.parametrize("above", [12.0, 14.0, 17.0])
+@pytest.mark.parametrize("kv_len,q_len", [([4000], [1]), ([4000, 900, 2500], [1, 2, 1]), ([2000, 1500], [1, 1]),
+                                          ([4000, 900], [40, 130])])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_key_far_above_the_others_with_a_small_value(q, above, kv_len, q_len, dtype):  # noqa: F811
+    """A first token that takes nearly all weight and has no value: the output is the sum of thousands of
+    small weights.  Beside the bounds of Case.check, fp16 weights of less than 2^-14 lie on a grid of 2^-24:
+    off by 2^-25 where the largest is at least 2^8 (many rows) or 2^15 (few), so by 2^-33 or 2^-40 of the largest
+    weight, which is at most 1.  bf16 has no such bound."""
+    D, H, Hkv = 64, 4, 2
+    c = Case(q, kv_len, q_len, H, Hkv, D, 32, dtype, seed=61, std=0.3)
+    c.qt[..., 0] = 8.0
+    for b, n in enumerate(kv_len):
+        k, v = c.kd[b].float(), c.vd[b].float() * 1000.0
+        k[:, :, 0] = 0.0
+        k[0] = 0.0
+        k[0, :, 0] = above
+        v[0] = 0.0
+        put(c, b, k, v)
+    c.run()
+    grid = 0.0 if dtype is torch.bfloat16 else 2.0 ** -40 if max(q_len) * (H // Hkv) <= 16 else 2.0 ** -33
+    eps = EPS[dtype]
+    p16 = eps / 2 if max(q_len) * (H // Hkv) > 16 else 2.0 ** -16
+    out, lse, qn = np64(c.out), np64(c.lse), np64(c.qt)
+    for b, n in enumerate(q_len):
+        k, v = np64(c.kd[b]), np64(c.vd[b])
+        for i in {0, n // 2, n - 1}:
+            at = slice(int(c.cu[b]) + i, int(c.cu[b]) + i + 1)
+            x = kv_len[b] - n + i
+            want, wl, mag = serve.attention(qn[at], k, v, x, D ** -0.5)
+            top = max((np.abs(qn[at][0, h]) * np.abs(k[:, h // (H // Hkv)])).sum(-1).max() for h in range(H))
+            d = D ** -0.5 * D * 2.0 ** -24 * top + 2.0 ** -18
+            small = grid * np.repeat(np.abs(v[:x + 1]).sum(0), H // Hkv, 0)[None]
+            err = np.abs(out[at] - want)
+            tol = eps / 2 * np.abs(want) * (1 + eps) + (2 * d + p16) * mag + small
+            assert (err <= tol).all(), (b, i, float((err / tol).max()))
+            assert (np.abs(lse[at] - wl) <= d + 2.0 ** -20 * np.abs(wl)).all(), (b, i)
