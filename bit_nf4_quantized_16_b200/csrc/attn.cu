@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
         }
     }
     if (row >= rows) return;
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = inverse_sum(L);
     const int g = d.row0 + row0 + row, tok = v.token_of(g);
     const int64_t orow = (int64_t)(d.q0 + tok) * v.heads + d.h * v.group + g - tok * v.group;
     const int64_t at = orow * v.head_dim + lane * V;
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(const __grid_constant
                 a[k].w += f * x.w;
             }
         }
-        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const float inv = inverse_sum(L);
 #pragma unroll
         for (int k = 0; k < DP / 32; k++)
             rows_out[lane][8 * k + warp] = make_uint2(pack2<F16>(a[k].x * inv, a[k].y * inv), pack2<F16>(a[k].z * inv, a[k].w * inv));

@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
             const int slot = 2 * (int)cta + (items == 0 ? 0 : 1), pr = h * 128 + row;
             float *part = p.part + (int64_t)slot * C::kSlotFloats;
             const int64_t orow = valid ? tensor_row(it, pr) : 0;
-            const float inv = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+            const float inv = whole ? inverse_sum(l) : 1.0f;
             if (has) {
                 ok = chunk_wait(&bars->o_full[h], n_o, bars, p);
                 ok = __all_sync(0xffffffffu, ok);

@@ -79,13 +79,17 @@ struct AttnParams {
 template <bool F16> constexpr int kRaiseFew = F16 ? 15 : 0;
 template <bool F16> constexpr int kRaiseMany = F16 ? 8 : 0;
 
-// log sum exp of a row from its reference and the sum of its weights.
+// log sum exp of a row from its reference and the sum of its weights.  A sum of 0 is that of a row that sees
+// nothing: with a key of finite score the largest weight alone is at least 1.  NaN stays NaN.
 template <int RAISE>
 __device__ __forceinline__ float log_sum(float ref, float sum, float scale_log2)
 {
     constexpr float kLower = 1.0f / (float)(1 << RAISE);
-    return sum > 0.0f ? __fmaf_rn(ref, scale_log2, log2f(sum * kLower)) * 0.69314718056f : -INFINITY;
+    return sum == 0.0f ? -INFINITY : __fmaf_rn(ref, scale_log2, log2f(sum * kLower)) * 0.69314718056f;
 }
+
+// What a row's output is multiplied with in the end.
+__device__ __forceinline__ float inverse_sum(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 
 struct Request {
     int q0, qn;   // rows of the batch's tensors [q0, q0 + qn)

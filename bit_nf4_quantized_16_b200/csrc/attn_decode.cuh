@@ -426,7 +426,8 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
 #pragma unroll
                 for (int w = 0; w < C::kWarps; w++) {
                     const float mw = stat[w * 32 + r];
-                    L += mw == -INFINITY ? 0.0f : exp2f((mw - M) * p.scale_log2) * stat[w * 32 + 16 + r];
+                    const float f = mw == -INFINITY ? 0.0f : exp2f((mw - M) * p.scale_log2);
+                    L += f * stat[w * 32 + 16 + r];   // (a product: a sum of NaN shows in L even where no score was a number)
                 }
                 stat[r] = M;
                 stat[16 + r] = L;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                     a.z += f * x.z;
                     a.w += f * x.w;
                 }
-                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+                const float inv = inverse_sum(L);
                 const int g = gr0 + r, t = v.token_of(g);
                 const int64_t row = (int64_t)(it.r.q0 + t) * v.heads + it.h * v.group + g - t * v.group;
                 const int64_t at = row * v.head_dim + c;
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP>::kThreads, 2) decode_kernel(cons
                 a.w += f * x.w;
             }
             if (it.whole) {
-                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+                const float inv = inverse_sum(L);
                 const int g = gr0 + r;
                 const int64_t row = (int64_t)(it.r.q0 + v.token_of(g)) * v.heads + it.h * v.group + g - v.token_of(g) * v.group;
                 const int64_t at = row * v.head_dim + c;

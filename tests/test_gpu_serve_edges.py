@@ -100,3 +100,31 @@ def test_a_key_far_above_the_others_with_a_small_value(q, above, kv_len, q_len, 
             tol = eps / 2 * np.abs(want) * (1 + eps) + (2 * d + p16) * mag + small
             assert (err <= tol).all(), (b, i, float((err / tol).max()))
             assert (np.abs(lse[at] - wl) <= d + 2.0 ** -20 * np.abs(wl)).all(), (b, i)
+
+
+@pytest.mark.parametrize("kv_len,q_len,heads", [([700], [1], 8), ([700, 500], [1, 1], 8), ([9000, 20, 300], [1, 1, 1], 8),
+                                                ([700, 500], [40, 40], 8), ([9000], [40], 4)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("what", ["nan row", "inf row", "inf in a row", "nan key"])
+def test_lse_of_a_row_that_is_not_finite(q, kv_len, q_len, heads, D, what):  # noqa: F811
+    """-inf is kept for rows that see nothing: a row without a finite result has none in lse either."""
+    c = Case(q, kv_len, q_len, heads, 2, D, 16, seed=62).run()
+    first = c.lse.clone()
+    hit = torch.zeros(c.T, heads, dtype=torch.bool, device="cuda")
+    hit[0, 3] = True
+    if what == "nan row":
+        c.qt[0, 3] = math.nan
+    elif what == "inf row":
+        c.qt[0, 3] = math.inf
+    elif what == "inf in a row":
+        c.qt[0, 3, 1] = math.inf
+    else:       # position 3 of the first request, key/value head 1: seen by all its rows
+        c.cache.k[int(c.table[0, 0]), 1, 3] = math.nan
+        hit[0, 3] = False
+        hit[:q_len[0], heads // 2:] = True
+    c.run()
+    assert not torch.isfinite(c.out[hit].float()).any()
+    assert not (torch.isfinite(c.lse[hit]) | torch.isneginf(c.lse[hit])).any()
+    # the others up to the bound of each call: the same products, maybe against another reference
+    others = ~hit
+    assert ((c.lse - first).abs() <= 2.0 ** -10 + 2.0 ** -19 * first.abs())[others].all()
