@@ -19,19 +19,20 @@ namespace {
 // One cluster of CTAs.  Every CTA scans all requests (three prefix sums: rows,
 // pages returned, pages taken), so that any of them can answer for any page or
 // token with a binary search in its shared memory; then the CTAs divide the
-// outputs.  Page j of the pool is free_pages[j] below the old count and a page
-// of an ended request above it, read from that request's row of the table,
-// which this call does not change: no CTA reads what another one writes.  Only
-// the count may be updated in place: it is read before the cluster's barrier
-// and written after it.
+// outputs.  An ended request returns those of its entries that are pages (a caller
+// under a window may have given others away), so they are counted before the scan, a
+// warp a request.  If any are returned, the CTAs push them first and meet at the cluster's
+// barrier; from there on the pool is read only.  The count may be updated in
+// place: it is read before the barrier at the end and written after it.
 //
 // The call moves a few hundred KB at most; what bounds it is latency (a launch,
 // three dependent reads, two scans), so a small batch gets one small CTA and a large
 // one as many threads as a cluster has; a thread takes four neighbouring
 // tokens, which mostly share the search.
-// Measured (B200): 16 requests of one token 4.8 us (append_kernel, which only streams,
-// takes 2.6 at its smallest); 1000 requests with 20651 tokens, 5937 returned and 1308
-// taken pages 11.4 us, of which the scans are a third.
+// Measured (B200, replayed): 16 requests of one token 4.0 us (append_kernel, which only
+// streams, takes 2.6 at its smallest); 1000 requests with 20651 tokens, 5937 returned and
+// 1308 taken pages 12.4 us, 7.5 without a returned one; with 300 ended requests 22 us.  (With one load
+// at a time in the count and the push: 17.6 and 31.)
 
 struct PlanParams {
     const int32_t *ctx, *qlen;
@@ -110,6 +111,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
     const int count = min(max(*p.free_count, 0), p.num_pages);
     auto pages = [&](int64_t t) { return (t + page - 1) >> p.page_shift; };
     const int64_t capacity = (int64_t)p.max_pages << p.page_shift;
+    auto is_page = [&](int32_t id) { return (unsigned)id < (unsigned)p.num_pages; };
+    constexpr int kAtOnce = 16;   // loads of a lane that do not wait for one another
+    const int lane = tid & 31;
 
     Two at{0, 0};            // rows and returned pages so far
     int64_t take_at = 0;
@@ -117,7 +121,22 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
         const int b = b0 + tid;
         const int64_t ctx = b < n ? p.ctx[b] : 0, q = b < n ? p.qlen[b] : 0;
         const int64_t rows = max(q, (int64_t)0);
-        const int64_t back = q < 0 ? min(pages(max(ctx, (int64_t)0)), (int64_t)p.max_pages) : 0;
+        const int held = q < 0 ? (int)min(pages(max(ctx, (int64_t)0)), (int64_t)p.max_pages) : 0;
+        int64_t back = 0;
+        for (unsigned left = __ballot_sync(0xffffffffu, held > 0); left; left &= left - 1) {
+            const int l = __ffs(left) - 1, entries = __shfl_sync(0xffffffffu, held, l);
+            const int32_t *row = p.table + (int64_t)(b - lane + l) * p.max_pages;
+            int found = 0;
+            for (int i0 = 0; i0 < entries; i0 += 32 * kAtOnce) {
+                int32_t id[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; k++) id[k] = i0 + 32 * k + lane < entries ? row[i0 + 32 * k + lane] : -1;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; k++) found += is_page(id[k]);
+            }
+            found = __reduce_add_sync(0xffffffffu, found);
+            if (lane == l) back = found;
+        }
         Two total;
         const Two pre = block_scan(Two{rows, back}, warp_sum, total);
         const int64_t rows0 = at.a + pre.a, back0 = at.b + pre.b;
@@ -150,13 +169,27 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
         if (take_pre[mid] <= pool) lo = mid; else hi = mid;
     }
     const int used = take_pre[lo];
-    // where the id of page j of the pool stands
-    auto pool_page = [&](int j) -> const int32_t * {
-        if (j < count) return p.free_pages + j;
-        const int r = j - count, b = owner_of(back_pre, n, r);
-        const int64_t i = (int64_t)b * p.max_pages + r - back_pre[b];
-        return QLORA_IN(i, (int64_t)n * p.max_pages) ? p.table + i : p.table;
-    };
+    if (returned > 0) {   // the same in every CTA
+        const int warps = (int)(step >> 5);
+        for (int b = (int)(first >> 5); b < n; b += warps) {   // a warp a request, its pages in their order
+            int to = back_pre[b];
+            const int end = min(back_pre[b + 1], returned);
+            const int32_t *row = p.table + (int64_t)b * p.max_pages;
+            for (int i0 = 0; to < end && i0 < p.max_pages; i0 += 32 * kAtOnce) {
+                int32_t id[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; k++) id[k] = i0 + 32 * k + lane < p.max_pages ? row[i0 + 32 * k + lane] : -1;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; k++) {
+                    const unsigned found = __ballot_sync(0xffffffffu, is_page(id[k]));
+                    const int at = to + __popc(found & ((1u << lane) - 1));
+                    if (is_page(id[k]) && at < end && QLORA_IN(count + at, p.num_pages)) p.free_pages[count + at] = id[k];
+                    to += __popc(found);
+                }
+            }
+        }
+        if (ctas > 1) sm100::cluster_sync(); else __syncthreads();
+    }
     // Whether request b, which fits, gets its pages.  (The prefix counts what refused requests
     // asked for too; that is at most tokens / 16 + batch pages, so it stays in 32 bits.)
     auto granted = [&](int b) { return take_pre[b + 1] == take_pre[b] || take_pre[b + 1] <= pool; };
@@ -167,12 +200,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
         const bool ok = ctx_of[b] >= 0 && granted((int)b);
         p.kv_len[b] = ok ? ctx_of[b] + max(p.qlen[b], 0) : 0;
     }
-    for (int64_t r = first; r < returned; r += step)
-        if (QLORA_IN(count + r, p.num_pages)) p.free_pages[count + r] = *pool_page((int)(count + r));
     for (int64_t u = step - 1 - first; u < used; u += step) {   // (the last threads have the least to do below)
         const int b = owner_of(take_pre, n, (int)u);
         const int64_t i = (int64_t)b * p.max_pages + pages(ctx_of[b]) + u - take_pre[b];
-        if (QLORA_IN(i, (int64_t)n * p.max_pages)) p.table[i] = *pool_page(pool - 1 - (int)u);
+        if (QLORA_IN(i, (int64_t)n * p.max_pages)) p.table[i] = p.free_pages[pool - 1 - u];
     }
     const int all_rows = rows_pre[n];
     for (int64_t t4 = 4 * first; t4 < p.tokens; t4 += 4 * step) {
@@ -189,7 +220,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PlanParams p)
             if (ctx_of[b] < 0 || !granted(b)) continue;
             pos[k] = ctx_of[b] + t - rows_pre[b];
             const int held = (int)pages(ctx_of[b]), i = pos[k] >> p.page_shift;
-            id_at[k] = i < held ? p.table + (int64_t)b * p.max_pages + i : pool_page(pool - 1 - (take_pre[b] + i - held));
+            id_at[k] = i < held ? p.table + (int64_t)b * p.max_pages + i
+                                : p.free_pages + (pool - 1 - (take_pre[b] + i - held));
         }
 #pragma unroll
         for (int k = 0; k < 4; k++) slot[k] = id_at[k] ? *id_at[k] : -1;

@@ -563,9 +563,11 @@ typedef struct {
  * qlora_kv_plan -- block tables, slots and positions from the requests'
  * lengths, built on the GPU.
  *   ctx_len     device [batch], positions that request b holds already; its
- *               first ceil(ctx_len / page_size) table entries are its pages.
+ *               first ceil(ctx_len / page_size) table entries are its pages.  A
+ *               caller that has given pages before a window to others has set their entries to -1.
  *   q_len       device [batch], its new tokens (0: none this step); negative: the
- *               request has ended and its pages go back to the pool.
+ *               request has ended and its pages go back to the pool: those of its entries
+ *               that are in [0, num_pages).
  *   free_pages  device [num_pages], the pool: a stack whose first
  *               *free_count entries are free page ids.  Returned pages are
  *               pushed (in the requests' order), then new pages are taken from
@@ -627,7 +629,8 @@ QLORA_API qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora_
  * beyond the table, are left out as if they were masked.  Under a window, pages
  * (pieces of 128 positions of larger ones) of which no row sees a position are
  * not used, whatever their entries say and they hold: a caller may have given
- * them to another request.  Elsewhere a position that a row does not see has weight 0 in
+ * them to another request (and sets their entries to -1, or qlora_kv_plan returns them once more when
+ * the request ends).  Elsewhere a position that a row does not see has weight 0 in
  * it; a value there that is not finite makes that NaN, as in any product.  Rows
  * of `out` at and after cu_q[batch] are left as they were.
  *   q, out  device [tokens][heads][head_dim] of the cache's type, tokens *

@@ -18,8 +18,9 @@ def plan(ctx, new, table, page, tokens, free, count):
     for b in range(B):
         if new[b] < 0:
             for i in range(min(pages(max(ctx[b], 0)), width)):
-                free_out[len(pool)] = table[b, i]
-                pool.append(int(table[b, i]))
+                if 0 <= table[b, i] < len(free_out):     # else: given away, or never a page
+                    free_out[len(pool)] = table[b, i]
+                    pool.append(int(table[b, i]))
     cu, kv_len = [0], []
     positions, slots = np.full(tokens, -1), np.full(tokens, -1)
     rows, exhausted = 0, False
@@ -36,7 +37,8 @@ def plan(ctx, new, table, page, tokens, free, count):
             for i in range(n):
                 x = ctx[b] + i
                 positions[rows + i] = x
-                slots[rows + i] = table[b, x // page] * page + x % page
+                if 0 <= table[b, x // page] < len(free_out):     # no slot on an entry that is no page
+                    slots[rows + i] = table[b, x // page] * page + x % page
         kv_len.append(ctx[b] + n if ok else 0)
         rows += n
         cu.append(min(rows, tokens))

@@ -128,3 +128,43 @@ def test_lse_of_a_row_that_is_not_finite(q, kv_len, q_len, heads, D, what):  # n
     # the others up to the bound of each call: the same products, maybe against another reference
     others = ~hit
     assert ((c.lse - first).abs() <= 2.0 ** -10 + 2.0 ** -19 * first.abs())[others].all()
+
+
+@pytest.mark.parametrize("seed", range(5))
+def test_plan_returns_only_entries_that_are_pages(q, seed):  # noqa: F811
+    """Requests under a window whose pages before it went to others: those entries hold -1 (or no page at all)
+    when the request ends, and only the rest goes back to the pool."""
+    rng = np.random.default_rng(100 + seed)
+    B, page = [3, 50, 400, 2000, 4096][seed], 16
+    width = [70, 30, 200, 12, 5][seed]
+    ctx = rng.integers(0, width * page + 1, B)
+    new = np.where(rng.random(B) < 0.4, -1, rng.integers(0, 2 * page, B))
+    new[rng.random(B) < 0.1] = -2 ** 31
+    pages = -(-ctx // page)
+    ids = rng.permutation(int(pages.sum()) + 50)
+    P, at = len(ids), 0
+    table = np.full((B, width), -1)
+    for b in range(B):
+        table[b, :pages[b]] = ids[at:at + pages[b]]
+        at += pages[b]
+        sinks, window = int(rng.integers(0, 3)), int(rng.integers(0, width))
+        if rng.random() < 0.7:      # given away: page ids below `given` are taken to be the pool's again
+            table[b, sinks:max(sinks, pages[b] - window)] = rng.choice([-1, P, 2 ** 31 - 1, -2 ** 31])
+    held = table[(table >= 0) & (table < P)]
+    free = np.full(P, -1)
+    rest = np.setdiff1d(np.arange(P), held)
+    free[:len(rest)] = rest
+    tokens = int(np.maximum(new, 0).sum()) + 5
+    want = serve.plan(ctx, new, table, page, tokens, free, len(rest))
+    kv = q.KVBatch(B, width, tokens, block_table=i32(table))
+    fp, fc = i32(free), i32([len(rest)])
+    q.qlora_kv_plan(kv, page, P, i32(ctx), i32(new), fp, fc)
+    q.qlora_check_device_error()
+    for name in ("block_table", "cu_q", "kv_len", "positions", "slots"):
+        assert np.array_equal(getattr(kv, name).cpu().numpy(), want[name]), name
+    assert int(fc) == want["free_count"] and np.array_equal(fp.cpu().numpy(), want["free_pages"])
+    # every page is in the pool or in one live row, once
+    live = want["block_table"][(new >= 0)]
+    mine = np.concatenate([want["free_pages"][:want["free_count"]], live[(live >= 0) & (live < P)]])
+    assert len(np.unique(mine)) == len(mine)
+    assert (want["free_pages"][:want["free_count"]] >= 0).all()
