@@ -521,7 +521,20 @@ def _cuda_index(t):
     return t.get_device()
 
 
-class KVCache:
+class _Described:
+    """Holds the descriptor that the calls read and the tensors whose addresses it has:
+    what went into it cannot be replaced, or a call would go on with the old ones."""
+
+    _open = ()      # names that may be set again; see the class's own __setattr__
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__ and name not in self._open:
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be set: write into the tensors, or make a new "
+                                 f"{type(self).__name__}")
+        object.__setattr__(self, name, value)
+
+
+class KVCache(_Described):
     """A layer's paged cache over the caller's tensors k and v of shape
     [num_pages, kv_heads, page_size, head_dim] (any order of the first three
     dimensions in memory, both alike; head_dim contiguous)."""
@@ -543,10 +556,18 @@ class KVCache:
         return KVCache(k, torch.empty_like(k))
 
 
-class KVBatch:
+class KVBatch(_Described):
     """A step's batch (see qlora_kv_batch in qlora.h): int32 arrays that
     qlora_kv_plan fills.  Arrays that are not given are made, on the device
-    of those that are (or `device`)."""
+    of those that are (or `device`).  max_q_len may be set again; it takes part in
+    the size of the workspace."""
+
+    _open = ("max_q_len",)
+
+    def __setattr__(self, name, value):
+        if name == "max_q_len" and "_ref" in self.__dict__:
+            self.desc.max_q_len = value
+        super().__setattr__(name, value)
 
     def __init__(self, batch: int, max_pages: int, tokens: int, max_q_len: int = 0, block_table=None, cu_q=None,
                  kv_len=None, positions=None, slots=None, device=None):

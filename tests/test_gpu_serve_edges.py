@@ -168,3 +168,28 @@ def test_plan_returns_only_entries_that_are_pages(q, seed):  # noqa: F811
     mine = np.concatenate([want["free_pages"][:want["free_count"]], live[(live >= 0) & (live < P)]])
     assert len(np.unique(mine)) == len(mine)
     assert (want["free_pages"][:want["free_count"]] >= 0).all()
+
+
+def test_what_a_descriptor_holds_cannot_be_replaced(q):  # noqa: F811
+    """The calls read addresses and sizes from the descriptor: a tensor set in its place would be
+    ignored, and the old one's memory, free by then, used."""
+    cache, kv = q.KVCache.empty(4, 16, 2, 64), q.KVBatch(2, 3, 10, max_q_len=1)
+    for thing, names in ((cache, ("k", "v", "desc", "device", "num_pages", "page_size", "dtype")),
+                         (kv, ("block_table", "cu_q", "kv_len", "positions", "slots", "batch", "max_pages", "tokens",
+                               "desc"))):
+        for name in names:
+            before = getattr(thing, name)
+            with pytest.raises(AttributeError):
+                setattr(thing, name, before.clone() if isinstance(before, torch.Tensor) else before)
+            assert getattr(thing, name) is before
+
+
+def test_max_q_len_set_again_reaches_the_calls(q):  # noqa: F811
+    """It chooses the kernel, and with it the workspace."""
+    few, many = [Case(q, [300, 40], [1, 1], 8, 4, 128, 16, seed=63, pad=30, max_q_len=n) for n in (1, 31)]
+    size = lambda c: q.qlora_paged_attn_workspace_bytes(c.cache, c.kv, 8)   # noqa: E731
+    assert size(few) != size(many)
+    few.run()
+    many.kv.max_q_len = 1
+    assert many.kv.max_q_len == 1 and size(few) == size(many)
+    assert torch.equal(many.run().out, few.out)
