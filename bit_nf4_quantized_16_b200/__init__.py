@@ -660,5 +660,5 @@ def qlora_block_fwd_cached(block: Block, cache: KVCache, kv: KVBatch, rope, x, y
     xp, yp = _is(x, torch.bfloat16, shape, dev, "x"), _is(y, torch.bfloat16, shape, dev, "y")
     _need(xp != yp, "y may not be x")
     _on(dev, stream, lib.qlora_block_fwd_cached,
-        (ctypes.addressof(block.desc), cache._ref, kv._ref, ctypes.addressof(rope), xp, yp, window, sinks,
+        (ctypes.addressof(block.desc), cache._ref, kv._ref, None if rope is None else ctypes.addressof(rope), xp, yp, window, sinks,
          workspace.data_ptr(), workspace.nbytes), "qlora_block_fwd_cached")

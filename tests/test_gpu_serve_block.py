@@ -152,3 +152,14 @@ def test_a_missing_adapter_is_refused_before_anything_is_written(q):
     assert e.value.status == 1
     torch.cuda.synchronize()
     assert not cache.k.any() and not cache.v.any() and (y == 7.0).all()
+
+
+def test_no_rope_is_refused(q):
+    case = synthetic.block_case(1, 16, 256, 2, 512, 16, alpha=16.0, seed=2900)
+    blk = build(q, case)
+    cache, kv = q.KVCache.empty(4, 16, 2, 128), q.KVBatch(1, 4, 16)
+    ws = torch.empty(q.qlora_block_cached_workspace_bytes(blk, cache, kv), dtype=torch.uint8, device="cuda")
+    x = case["x"].cuda()
+    with pytest.raises(q.QLoraError) as e:
+        q.qlora_block_fwd_cached(blk, cache, kv, None, x, torch.empty_like(x), ws)
+    assert e.value.status == 1
