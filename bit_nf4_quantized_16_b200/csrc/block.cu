@@ -397,7 +397,6 @@ extern "C" qlora_status qlora_block_fwd_cached(const qlora_block *b, const qlora
     if (!attn) return QLORA_ERR_SHAPE;
     for (int l = 0; l < kL; l++) {
         QLORA_TRY(check_weight(&b->w[l]));
-        if (!b->A[l] || !b->B[l]) return QLORA_ERR_INVALID_ARG;
         if (!aligned16(b->A[l]) || !aligned16(b->B[l])) return QLORA_ERR_ALIGNMENT;
     }
     Ctx c{b, layout_cached(b, kv->tokens, attn), static_cast<char *>(workspace), static_cast<cudaStream_t>(stream),

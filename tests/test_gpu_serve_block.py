@@ -163,3 +163,24 @@ def test_no_rope_is_refused(q):
     with pytest.raises(q.QLoraError) as e:
         q.qlora_block_fwd_cached(blk, cache, kv, None, x, torch.empty_like(x), ws)
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("which", ["A", "B"])
+def test_a_misaligned_adapter_is_refused_before_anything_is_written(q, which):
+    """The last linear's: the first six would have run, and the cache been written."""
+    case = synthetic.block_case(1, 16, 256, 2, 512, 16, alpha=16.0, seed=3000)
+    blk = build(q, case)
+    cache, kv, rope = q.KVCache.empty(4, 16, 2, 128), q.KVBatch(1, 4, 16), q.qlora_build_rope(128)
+    ws = torch.empty(q.qlora_block_cached_workspace_bytes(blk, cache, kv), dtype=torch.uint8, device="cuda")
+    for t in (cache.k, cache.v):
+        t.zero_()
+    kv.slots.copy_(torch.arange(16, dtype=torch.int32))
+    kv.positions.copy_(torch.arange(16, dtype=torch.int32))
+    x = case["x"].cuda()
+    y = torch.full_like(x, 7.0)
+    getattr(blk.desc, which)[6] += 8
+    with pytest.raises(q.QLoraError) as e:
+        q.qlora_block_fwd_cached(blk, cache, kv, rope, x, y, ws)
+    assert e.value.status == 3
+    torch.cuda.synchronize()
+    assert not cache.k.any() and not cache.v.any() and (y == 7.0).all()
