@@ -396,8 +396,8 @@ qlora_status check_cache(const qlora_kv_cache *c)
     std::sort(order, order + 3, [&](int a, int b) { return st[a] < st[b]; });
     int64_t reach = c->head_dim;
     for (int i : order) {
+        if (n[i] == 1) continue;   // its stride is never used
         if (st[i] % 8 || st[i] < 0 || st[i] >= ((int64_t)1 << 39) / 2) return QLORA_ERR_SHAPE;
-        if (n[i] == 1) continue;
         if (st[i] < reach) return QLORA_ERR_SHAPE;
         reach = st[i] * (n[i] - 1) + reach;
     }

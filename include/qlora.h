@@ -524,7 +524,7 @@ QLORA_API qlora_status qlora_linear_adapter_bwd(const qlora_nf4_weight *w, const
  * with head_dim contiguous values; both orders of heads and positions are
  * served.  page_size: a power of two, 16 to 256.  num_pages * page_size <=
  * 2^31 - 1.  head_dim: a multiple of 16, 16 to 128.  Strides: multiples of 8,
- * such that no two rows overlap.  dtype: QLORA_BF16 or QLORA_FP16, also the type of q,
+ * such that no two rows overlap (that of a dimension of one may be anything).  dtype: QLORA_BF16 or QLORA_FP16, also the type of q,
  * k, v and the output.  Pages need not be initialized: what lies at or
  * beyond a request's length is never used, whatever it holds.
  */

@@ -142,3 +142,17 @@ def test_attention_arguments(lib):  # noqa: F811
     n = lib.qlora_paged_attn_workspace_bytes
     n.restype, n.argtypes = S, [P, P, I32]
     assert n(ctypes.byref(cache(page_size=8)), ctypes.byref(batch()), 4) == 0
+
+
+@needs_no_gpu
+def test_a_dimension_of_one_has_any_stride(lib):  # noqa: F811
+    """The stride of one head or one page is never used, and tensors of one carry all kinds: only
+    the device is missing."""
+    f = lib.qlora_kv_append
+    f.argtypes = [P, P, P, P, P, P, I32, P, P]
+    for kw in (dict(kv_heads=1, stride_head=1), dict(kv_heads=1, stride_head=-4), dict(num_pages=1, stride_page=3),
+               dict(num_pages=1, stride_page=2 ** 50), dict(kv_heads=1, stride_head=0, stride_page=1024)):
+        assert f(ctypes.byref(cache(**kw)), ctypes.byref(batch()), None, FAKE, FAKE, FAKE, 4, FAKE, None) in (5, 6), kw
+    # the others count as they did
+    assert f(ctypes.byref(cache(kv_heads=1, stride_head=1, stride_page=1000)), ctypes.byref(batch()), None, FAKE, FAKE,
+             FAKE, 4, FAKE, None) == 2

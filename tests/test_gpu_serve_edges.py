@@ -193,3 +193,18 @@ def test_max_q_len_set_again_reaches_the_calls(q):  # noqa: F811
     many.kv.max_q_len = 1
     assert many.kv.max_q_len == 1 and size(few) == size(many)
     assert torch.equal(many.run().out, few.out)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_one_head_of_an_odd_stride(q, n):  # noqa: F811
+    """The stride of a dimension of one is never used."""
+    c = Case(q, [200, 50], [n, 2], 4, 1, 64, 16, seed=64)
+    odd = lambda t: t.as_strided(t.shape, (t.stride(0), 3, t.stride(2), 1))   # noqa: E731
+    c.cache = q.KVCache(odd(c.cache.k), odd(c.cache.v))
+    assert c.cache.desc.stride_head == 3
+    c.run().check()
+    x = torch.randn(c.T, 1, 64, device="cuda").to(torch.bfloat16)
+    q.qlora_kv_append(c.cache, q.KVBatch(1, 1, c.T, slots=torch.arange(c.T, dtype=torch.int32, device="cuda")), None,
+                      c.qt, x, -x)
+    flat = c.cache.k.transpose(1, 2).reshape(-1, 1, 64)
+    assert torch.equal(flat[:c.T], x)
