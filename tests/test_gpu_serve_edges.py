@@ -208,3 +208,27 @@ def test_one_head_of_an_odd_stride(q, n):  # noqa: F811
                       c.qt, x, -x)
     flat = c.cache.k.transpose(1, 2).reshape(-1, 1, 64)
     assert torch.equal(flat[:c.T], x)
+
+
+@pytest.mark.parametrize("kv_heads,lengths,window,sinks,launches", [
+    (16, [0, 1, 16, 65, 300, 700, 1000, 1200], 0, 0, 1),        # two CTAs a head: 128 heads, a table of 1200 positions
+    (16, [0, 1, 16, 65, 300, 2000, 4000, 5000], 900, 20, 1),    # ... or a window
+    (25, [0, 1, 16, 65, 300, 500, 620, 640], 0, 0, 1),          # one: 200 heads, a table of 640
+    (25, [0, 1, 16, 65, 300, 2000, 4000, 5000], 1000, 4, 1),
+    (25, [0, 1, 16, 65, 300, 700, 1000, 1200], 0, 0, 2),        # a longer table: the schedule and its join
+    (38, [0, 1, 16, 65, 300, 500, 620, 640], 0, 0, 2)])         # 304 heads
+def test_forms_of_few_requests(q, kv_heads, lengths, window, sinks, launches):  # noqa: F811
+    """Requests without rows, without keys, and (promised to be short) with several tiles of rows."""
+    if torch.cuda.get_device_properties(0).multi_processor_count != 148:
+        pytest.skip("the counts are those of 148 SMs")
+    for new in ([1, 0, 1, 1, 2, 1, 1, 1], [1, 1, 9, 20, 0, 30, 1, 3]):
+        c = Case(q, lengths, new, 2 * kv_heads, kv_heads, 64, 16, seed=65, max_q_len=2)
+        n = q.qlora_launch_count()
+        c.run(window, sinks)
+        assert q.qlora_launch_count() - n == launches
+        c.check(window, sinks)
+
+
+@pytest.mark.parametrize("kv", [1, 70, 900])
+def test_one_request_of_more_heads_than_places(q, kv):  # noqa: F811
+    Case(q, [kv], [1], 320, 320, 16, 16, seed=66).run().check()
