@@ -152,13 +152,21 @@ size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
 // CTAs per key/value head of the cluster form, or 0: not used.  The form gives
 // every head of every request the same number of CTAs, whatever the lengths are (the
-// host does not know them).  It saves 4 to 5 us a call where the requests are alike (4
-// requests of 3000 positions, 8 heads of 128: 13.5 us for 17.4; 500 positions of one request
-// with 32 heads: 6.8 for 11.2; 30000: 77 for 83) and loses up to 6 where they are not
-// (8 requests of 100 to 4000 positions: 23.7 for 17.4).  So it is taken for one
-// request alone that fills the device, and otherwise where a CTA reads few positions:
-// at most kWindowed under a window, which evens the lengths out (32 requests,
-// window 1024: 29.3 us for 34.6), or kOpen without one.
+// host does not know them).  It saves 4 to 6 us a call where the requests are alike (500
+// positions of one request with 32 heads: 6.8 us for 11.2; 30000: 77 for 83) and loses
+// where one is much longer than the others.  So it is taken for one request alone that
+// fills the device, and otherwise where a CTA reads few positions: at most kOpen, or
+// under a window kWindowed.  Its time over that of the schedule, by positions a CTA at most,
+// measured with 32, 16, 8 and 4 requests of 8 heads of 128 (256 of 296 places taken):
+//   positions                          320         640         960         1280        2560
+//   no window, all alike            .71 to .77  .77 to .82  .84 to .86  .86 to .89  .89 to .93
+//   no window, spread evenly        .73 to .82  .83 to .91  .91 to 1.1  .97 to 1.1  1.1 to 1.2
+//   no window, one long, others 5%  .72 to .83  .89 to 1.1  1.0 to 1.4  1.1 to 1.7  1.5 to 2.4
+//   positions of the window            256         512        1024        1280        2048        4096
+//   all contexts beyond it          .73 to .80  .79 to .83  .86 to .88  .85 to .90  .92 to .94  .93 to .95
+// With half the places taken (2 requests) the last line is .76, .89, .98, 1.04 and 1.13 up to 2048.  A
+// window evens lengths out only where contexts exceed it: with one long request and short
+// others the third line holds for it too.
 constexpr int64_t kWindowed = 1280, kOpen = 640;
 int cluster_ctas(const AttnParams &p, const DeviceInfo &dev)
 {

@@ -33,12 +33,18 @@
 // row's largest, 2^-33 of that); sums are
 // taken of the unrounded fp32 weights.
 //
-// Measured (B200, 1965 MHz; on another one at 1.66 GHz a prompt takes 177 us).  2048 tokens over 16000 positions, 32 heads of 128: 530 to
-// 550 us, 1030 to 1090 TFLOP/s (0.61 to 0.65 of the measured GEMM rate); a whole prompt of
-// 4096 tokens: 152 to 156 us; heads of 64: 650 TFLOP/s.  A tile of both halves takes 4080
-// cycles: its 32 products take 90 cycles each (2880; that is the GEMM rate), a half's softmax
-// 1500 on its own (1024 of them the exponentials, 16 a cycle and SM), and a half
-// waits for both in turn, since tensor memory has no room for a second S of 128 columns.
+// Measured (B200, by box: clocks under this kernel were 1.66 to 1.97 GHz).  2048 tokens over 16000 positions,
+// 32 heads of 128, at the highest clock: 530 to 550 us, 1030 to 1090 TFLOP/s (0.61 to 0.65 of the measured
+// GEMM rate).  A whole prompt of 4096 tokens, 32 heads of 128: 152 to 176 us, 780 TFLOP/s at the last (0.46).
+// Four chunks of 1500 to 2048 tokens, window 1024: 219 to 254 us (0.28 to 0.32 of that rate: whole tiles are
+// computed at the window's ends).  Seven ragged chunks, heads of 64: 61 us (0.21; 9 tiles an item).
+// The prompt's 57 tiles an SM take 258,000 cycles, 4500 each.  By the counters the tensor pipe is
+// busy for 2050 of them (64 for each of the 32 products) and the exponentials' for 2050 (16 a
+// cycle and SM).  A half needs 1020 cycles of products and 1500 of softmax (measured alone), in turn;
+// the other 1900 are hand-overs and waiting between the warps, not told apart further.
+// The references and the raised fp16 weights (see attn_common.cuh) cost, on one box: prompt 166 to 168 us
+// (fp16 168 to 172), windowed chunks 227 to 231 (fp16 229 to 254: the few sinks that a first tile holds
+// make a low reference, and the second tile is mostly formed twice).
 // Tried, and no faster: two threads per row (194 us for a prompt that took 159
 // at that time, and 169 for 157 later); S in steps of 64 columns with two buffers (184 for
 // 182, 221 with a group of warps for each buffer); a quarter of the exponentials by a
@@ -106,7 +112,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 
 // The products of this kernel.  Descriptors of one operand differ in the low
 // word only (the start address), so a step costs one addition: the issuing
-// thread has no time for more (90 cycles per product).
+// thread has no time for more (64 cycles per product).
 template <bool kAccumulate>
 __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc)
 {

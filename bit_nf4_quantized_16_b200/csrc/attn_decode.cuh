@@ -18,10 +18,11 @@
 // 16-bit p the output would carry its rounding beside the output's own.  The
 // products have time for it: 16 rows x 16 positions take 48 of them for 8 KB.
 //
-// Measured (B200): 16 requests of 4100 positions, 64 heads of 128 (2.1 GB): 316 us, 6.8 TB/s;
-// 64 requests of 100 to 16000 positions, 8 heads: 116 us, 6.0 TB/s (0.92 of the
-// measured copy rate); one request of 500 positions, 32 heads: 6.9 us, of which
-// launch, lengths, table and first copy are four dependent latencies.
+// Measured (B200, by box): 16 requests of 4100 positions, 64 heads of 128 (2.1 GB): 338 to 341 us,
+// 6.3 TB/s (0.96 of the measured copy rate); 64 requests of 100 to 16000 positions, 8 heads:
+// 121 us, 5.8 TB/s (0.88); one request of 500 positions, 32 heads: 7.4 us a call, of which
+// launch, lengths, table and first copy are four dependent latencies; 32 requests under a window of
+// 1024 with 4 sinks, 8 heads: 30.7 us, 4.4 TB/s (0.67: 256 whole items on 296 places, start and join around them).
 #pragma once
 #include <type_traits>
 
@@ -33,7 +34,7 @@ namespace attn {
 template <int DP>
 struct DecodeCfg {
     static constexpr int kWarps = 4, kThreads = 32 * kWarps;
-    static constexpr int kRows = 16, kTile = 16 * kWarps, kOv = 3;   // an item costs three tiles beside its own (64 ragged requests: 149 us with 0, 121 with 2, 116 with 3)
+    static constexpr int kRows = 16, kTile = 16 * kWarps, kOv = 3;   // an item costs three tiles beside its own (64 ragged requests on one box: 149 us with 0, 121 with 2, 116 with 3)
     static constexpr int kStages = DP == 128 ? 2 : 4;
     static constexpr uint32_t kStageBytes = 2 * 16 * DP * 2;   // keys, then values, of 16 positions
     static constexpr uint32_t kRing = kWarps * kStages * kStageBytes;

@@ -541,9 +541,9 @@ typedef struct {
  *   max_pages   width of the block table; max_pages * page_size <= 2^30.
  *   tokens      rows of q, k, v and the output (capacity: the requests' new
  *               tokens are packed from row 0, the rest is padding).
- *   max_q_len   no request has more new tokens than this; 0: not known.  It
- *               only steers which kernel is used, results do not depend on it
- *               beyond their rounding.
+ *   max_q_len   no request has more new tokens than this; 0: not known (then
+ *               `tokens` counts).  It steers which kernel is used and with it the rounding of
+ *               the weights (see qlora_paged_attn_fwd), and the workspace's size.
  *   block_table [batch][max_pages] page ids, request by request.
  *   cu_q        [batch + 1] first row of each request, and the rows' end.
  *   kv_len      [batch] positions of each request, its new tokens included.
@@ -639,11 +639,16 @@ QLORA_API qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora_
  *   window  0: none; else each row sees its last `window` positions (its own
  *           among them) and the first `sinks` of the request.
  *   lse     device float [tokens][heads] or NULL: log sum exp of the scores (-inf for a
- *           row that sees nothing).
+ *           row that sees nothing, NaN for one that sees a score of NaN or +inf).
  *   workspace  device, >= qlora_paged_attn_workspace_bytes, any content;
  *           calls that overlap in time need one each.
- * Softmax statistics and sums are fp32.  The division of work depends on the lengths
- * and the device only: the same call gives the same bits.
+ * Softmax statistics and sums are fp32.  With max_q_len * heads / kv_heads of at most 16 a weight
+ * enters the second product off by at most 2^-18 of itself (bf16) or 2^-22 of itself or 2^-40 of the row's
+ * largest (fp16); with more it is rounded to the type, half a step of itself (fp16: or 2^-33 of the
+ * row's largest).  A caller who wants the former for a batch with a long prompt calls for the
+ * prompt apart.  The division of work depends on the lengths, the sizes of the call (max_pages,
+ * tokens and max_q_len among them) and the device: the same call gives the same bits, the same
+ * requests in a wider table may be split otherwise.
  * Errors: INVALID_ARG, SHAPE, ALIGNMENT, WORKSPACE, CUDA, UNSUPPORTED; a bounded
  * wait that gave up is reported by qlora_check_device_error.
  */
