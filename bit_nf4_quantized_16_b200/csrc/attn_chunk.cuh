@@ -440,20 +440,28 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                 bool more = true, crossed = false;   // is there a tile for S; is it of another item than PV's
                 uint32_t items = 0;                  // items begun
                 int st = -1, s_end = 0;
-                auto next_tile = [&]() {
-                    crossed = false;
-                    st++;
-                    while (st >= s_end) {
-                        if (items) mbar_arrive(&bars->item_empty[(items - 1) & 3]);
-                        const ChunkItem *it = item_at(items++);
-                        crossed = true;
-                        more = it != nullptr;
-                        if (!more) return;
-                        st = it->t0;
-                        s_end = it->t1;
+                auto next_item = [&]() {
+                    if (items) mbar_arrive(&bars->item_empty[(items - 1) & 3]);
+                    const ChunkItem *it = item_at(items++);
+                    more = it != nullptr;
+                    if (!more) return;
+                    st = it->t0;
+                    s_end = it->t1;
 #pragma unroll
-                        for (int h = 0; h < 2; h++) sr[h] = it->half[h].t;
-                    }
+                    for (int h = 0; h < 2; h++) sr[h] = it->half[h].t;
+                };
+                auto next_tile = [&]() {   // one item ahead at most: it may have none
+                    st++;
+                    crossed = st >= s_end;
+                    if (crossed) next_item();
+                };
+                // Past the items without a tile.  Not with a second product to issue: the schedule cannot
+                // publish the fourth item from here before this item's place is free, which is
+                // when its rows are written, behind that product.
+                auto skip_empty = [&]() {
+                    while (more && st >= s_end) next_item();
+                };
+                auto look = [&]() {
                     s_how = 0;
 #pragma unroll
                     for (int h = 0; h < 2; h++)
@@ -502,7 +510,9 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                     return s;
                 };
                 next_tile();
+                skip_empty();
                 if (more) {
+                    look();
                     const uint32_t ks = advance();
                     scores(0, ks);
                     scores(1, ks);
@@ -514,6 +524,7 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                     next_tile();
                     const uint32_t vs = advance();
                     if (!crossed) {
+                        look();
                         const uint32_t ks = advance();
                         values(0, p_how, vs);
                         if (ok) scores(0, ks);
@@ -527,7 +538,9 @@ __global__ void __launch_bounds__(384, 1) chunk_kernel(const __grid_constant__ A
                         if (ok) values(1, p_how, vs);
                         if (!ok) break;
                         tc_commit(&bars->kv_empty[vs]);
+                        skip_empty();
                         if (!more) break;
+                        look();
                         const uint32_t ks = advance();
                         if (ok) scores(0, ks);
                         if (ok) scores(1, ks);

@@ -232,3 +232,12 @@ def test_forms_of_few_requests(q, kv_heads, lengths, window, sinks, launches):  
 @pytest.mark.parametrize("kv", [1, 70, 900])
 def test_one_request_of_more_heads_than_places(q, kv):  # noqa: F811
     Case(q, [kv], [1], 320, 320, 16, 16, seed=66).run().check()
+
+
+@pytest.mark.parametrize("kv_len,n", [([1] * 12, 497), ([1, 0, 0] * 5, 497), ([300, 0, 0, 0, 0] * 3, 290), ([2, 0] * 8, 400)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (448, 300)])
+def test_many_items_without_a_key_between_others(q, kv_len, n, window, sinks):  # noqa: F811
+    """Long prompts that were refused (no positions), or rows before position 0: a CTA gets four and
+    more items without a tile after one that has one."""
+    c = Case(q, kv_len, [n] * len(kv_len), 68, 17, 16, 16, seed=67, max_q_len=n)
+    c.run(window, sinks).check(window, sinks, rows=[0, n // 2, n - 2, n - 1])
