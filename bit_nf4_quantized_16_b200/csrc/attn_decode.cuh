@@ -18,9 +18,9 @@
 // 16-bit p the output would carry its rounding beside the output's own.  The
 // products have time for it: 16 rows x 16 positions take 48 of them for 8 KB.
 //
-// Measured (B200, by box): 16 requests of 4100 positions, 64 heads of 128 (2.1 GB): 338 to 341 us,
-// 6.3 TB/s (0.96 of the measured copy rate); 64 requests of 100 to 16000 positions, 8 heads:
-// 121 us, 5.8 TB/s (0.88); one request of 500 positions, 32 heads: 7.4 us a call, of which
+// Measured (B200, by box): 16 requests of 4100 positions, 64 heads of 128 (2.1 GB): 320 to 341 us,
+// 6.3 to 6.7 TB/s (0.96 to 1.03 of the measured copy rate, which writes half of its bytes); 64 requests of 100 to
+// 16000 positions, 8 heads: 115 to 121 us, 5.8 to 6.1 TB/s (0.88 to 0.93); one request of 500 positions, 32 heads: 7.4 us a call, of which
 // launch, lengths, table and first copy are four dependent latencies; 32 requests under a window of
 // 1024 with 4 sinks, 8 heads: 30.7 us, 4.4 TB/s (0.67: 256 whole items on 296 places, start and join around them).
 #pragma once

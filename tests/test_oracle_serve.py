@@ -20,6 +20,15 @@ def test_plan_by_hand():
     assert r["slots"].tolist() == [39, 32, 33, 28, 29, 30, 31, -1, -1]
 
 
+def test_plan_leaves_out_entries_that_are_no_page():
+    # request 0 has ended; its second entry was given away, its third is no page of the ten
+    table = np.array([[9, -1, 10, 4], [-1, -1, -1, -1]])
+    r = serve.plan([16, 0], [-1, 9], table, 4, 9, np.array([1, 2, -1, -1, -1, -1, -1, -1, -1, -1]), 2)
+    assert r["free_pages"][:4].tolist() == [1, 2, 9, 4] and r["free_count"] == 1
+    assert r["block_table"].tolist() == [[9, -1, 10, 4], [4, 9, 2, -1]]
+    assert r["slots"].tolist() == [16, 17, 18, 19, 36, 37, 38, 39, 8]
+
+
 def test_plan_refuses_in_order():
     # two pages serve requests 0 and 1, one page request 0 only; request 2 needs none and is served either way
     args = [0, 0, 1], [4, 4, 1], np.array([[-1, -1], [-1, -1], [5, -1]]), 4, 20, np.array([3, 4, 0, 0, 0, 0])
